@@ -7,7 +7,8 @@ Three operators, each in a plain form (elementary torch operations in 32 bits,
              K/V appended and the attention mass per cached position accumulated
   evict      eviction from that cache by the accumulated mass, down to a budget
   beam       beam search's selection over beams and vocabulary, then the states
-             (token history, page tables, the partly filled last pages) reordered
+             (token history, page tables, the partly filled last pages) reordered:
+             full pages are shared, each beam goes on in a fresh page of its own
 """
 import math
 
@@ -358,10 +359,9 @@ def _run_beam(s):
         full, rest = lengths // page, lengths % page
         table = s["table"][row]
         cols = torch.arange(table.shape[1], device="cuda")[None]
-        partial = (cols == full[:, None]) & (rest > 0)[:, None]
         old = table.gather(1, full[:, None].clamp(max=table.shape[1] - 1))[:, 0].long()
-        new = torch.where(partial, s["fresh"][:, None], table)
-        used = cols < (full + (rest > 0))[:, None]
+        new = torch.where(cols == full[:, None], s["fresh"][:, None], table)
+        used = cols <= full[:, None]
         s["table_out"].copy_(torch.where(used, new, s["table_out"]))
         s["lengths_out"].copy_(lengths)
         fresh = s["fresh"].long()
@@ -406,7 +406,7 @@ def work(case):
     lo, hi = case["min_len"], case["max_len"]
     each = [lo + (hi - lo) * i // max(1, B - 1) if B > 1 else hi for i in range(B)]
     partial = sum(n % page for n in each) * K
-    entries = sum(-(-n // page) for n in each) * K
+    entries = sum(n // page + 1 for n in each) * K
     return {"bytes": B * K * V * size + 26.0 * B * K + 8.0 * B * K * (case["max_len"] + 1) + 8.0 * entries
             + 8.0 * B * K + 2.0 * row * case["layers"] * partial, "flops": 4.0 * B * K * V}
 
@@ -503,11 +503,12 @@ def _exact_beam(c, s):
         history.view(B * K, -1)[n] = s["history"].view(B * K, -1)[p]
         length = old_len[p]
         lengths[n] = length
-        row = old_table[p][: -(-length // page)]
+        row = old_table[p][: length // page]
         if length % page:
+            last = old_table[p][length // page]
             for x in kv:
-                x[:, fresh[n], : length % page] = x[:, row[-1], : length % page]
-            row[-1] = fresh[n]
+                x[:, fresh[n], : length % page] = x[:, last, : length % page]
+        row.append(fresh[n])
         table[n, : len(row)] = torch.tensor(row, dtype=torch.int32, device="cuda")
     return {"parent": parent, "token": token, "score": score, "done": done, "history": history,
             "table": table, "lengths": lengths, "k": kv[0].double(), "v": kv[1].double()}
