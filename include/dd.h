@@ -36,6 +36,12 @@
  *     error word read by dd_get_device_error().
  *   - No C++ exception crosses this interface.
  *   - Supported: d in {64, 128}; Hq % Hkv == 0; L >= 1; V >= 1; B >= 1.
+ *
+ * Beside the verification step, the operators of token-by-token decoding with the
+ * same heads and the same vocabulary: single-token attention over a paged cache
+ * (dd_paged_attention), what bounds that cache (dd_cache_evict), and beam search
+ * over it (dd_beam_select, dd_beam_reorder, dd_paged_fork). The pages have no
+ * counterpart; they serve a drafter or verifier that decodes one token at a time.
  */
 #ifndef DD_VERIFY_H_
 #define DD_VERIFY_H_
@@ -53,8 +59,9 @@ typedef enum {
   DD_ERR_UNSUPPORTED = 2,   /* valid but not implemented (e.g. d = 96) */
   DD_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
   DD_ERR_TIMEOUT = 4,       /* device: a bounded wait ran out (see dd_get_device_error) */
-  DD_ERR_BOUNDS = 5         /* device, checked builds only: an index check failed and the
-                               access was skipped (see dd_bounds_checked) */
+  DD_ERR_BOUNDS = 5         /* device: a length or page id of a paged cache was out of range
+                               (every build), or an index check of the checked build failed
+                               (see dd_bounds_checked); the access was skipped */
 } dd_status;
 
 typedef enum { DD_F32 = 0, DD_BF16 = 1 } dd_dtype;
@@ -337,7 +344,6 @@ dd_status dd_decide(
     const dd_row_stats* stats, int B, int L, int R, int pos_offset,
     uint8_t* decision, int32_t* new_tokens, uint8_t* accepted, void* stream);
 
-/* Human-readable name of a status. */
 /*
  * dd_select_seeds_ex -- dd_select_seeds with an adaptive set size ([COVER]
  * section 2 calls the seed set "small and adaptive"; the page gives no rule).
@@ -352,6 +358,197 @@ dd_status dd_select_seeds_ex(
     int B, int L, int k, float min_score, int32_t* seeds, uint8_t* is_seed, float* score,
     int32_t* count, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Token-by-token decoding over a paged K/V cache.
+ *
+ * A cache holds, for each of N sequences, `lengths[n]` token slots. Slot j of
+ * sequence n is row j % page_size of page page_table[n, j / page_size]; a row of a
+ * page is Hkv heads of d elements, in k and in v alike:
+ *   element (layer, page, row, head, e) at
+ *   layer * layer_stride + page * page_stride + row * token_stride + head * head_stride + e.
+ * Pages of one sequence lie anywhere in the pool, and sequences may share pages they
+ * only read. A page id below 0 is a hole: its slots are not read and take no part in
+ * the softmax. A page id of n_pages or more, or a length outside [0, max_len], is an
+ * error found on the device: it records DD_ERR_BOUNDS, the page counts as a hole, the
+ * length is clamped.
+ * Strides are in elements and whole multiples of 16 bytes; k and v are 16-byte
+ * aligned. page_size is any number from 1 on. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t layer_stride;  /* used by dd_paged_fork; the other calls take layers = 1 */
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int layers;
+  int n_pages;
+  int page_size;
+  int Hkv;
+  int d;
+  dd_dtype dtype;
+  const int32_t* page_table;  /* [N, max_pages], row stride table_stride */
+  int64_t table_stride;
+  int max_pages;
+} dd_paged_cache;
+
+/*
+ * dd_paged_attention -- attention of one new token per sequence over its cached
+ * slots, with the attention mass each slot receives:
+ *   s_hj = softmax_scale q_h . k_j      (kv head h / (Hq / Hkv), j < lengths[b], no hole)
+ *   out_h = sum_j softmax_j(s_hj) v_j,  lse_h = log sum_j e^{s_hj}
+ *   mass_out_j = mass_in_j + (1/Hq) sum_h softmax_j(s_hj)
+ * The mass is the single-token counterpart of dd_dualview_attention's d_in: what
+ * dd_cache_evict ranks by.
+ *
+ * q               [B,Hq,d], sequence stride q_stride (elements), dtype cache->dtype
+ * k_new, v_new    [B,Hkv,d], sequence stride new_stride: the new token's K / V, written
+ *                 to slot lengths[b] - 1 of the cache (lengths count it) and attended to
+ *                 like the rest; both NULL: the cache already holds every slot. That slot's
+ *                 page must be the sequence's own and must not be a hole (a hole: the
+ *                 token is dropped, like the page's other slots).
+ * lengths         [B] int32, slots per sequence, 0 .. max_len. 0 (a padded batch): nothing
+ *                 is read or appended, out = 0, lse = -inf; so too where every slot is a hole.
+ * max_len         bound on lengths, at most max_pages * page_size; sizes the launch and
+ *                 the workspace, not the result.
+ * softmax_scale   <= 0 selects 1/sqrt(d)
+ * out             [B,Hq,d] contiguous, dtype of q (required)
+ * lse             [B,Hq] fp32, natural log (may be NULL)
+ * mass_in, mass_out  [B, .] fp32, row stride mass_stride >= max_len. mass_out NULL: no
+ *                 masses. mass_in NULL: zero. mass_in == mass_out adds in place. With
+ *                 k_new, the appended slot's mass starts at 0 whatever mass_in holds
+ *                 there. Slots at or beyond a sequence's length are not written.
+ * workspace       device scratch of at least dd_paged_attention_workspace_size(...) bytes,
+ *                 256-byte aligned; contents on entry are ignored. Calls that share a
+ *                 workspace must not overlap on the GPU.
+ * Two sequences may not append to the same slot. K/V/Q values of readable slots are
+ * finite; whatever lies in slots that are not read (NaN too) has no effect.
+ * Results do not depend on timing: no atomics, sums in a fixed order.
+ * Errors: DD_ERR_INVALID_ARG for null required pointers, non-positive sizes, Hq % Hkv,
+ * misalignment, one of k_new / v_new, max_len or mass_stride out of range, a short
+ * workspace; DD_ERR_UNSUPPORTED for d not in {64,128}, B > 4096, Hq > 8192,
+ * max_len > 2^30, or 2^31 or more tiles of 64 slots in B * Hq * max_len.
+ */
+dd_status dd_paged_attention(
+    const void* q, int64_t q_stride, const void* k_new, const void* v_new, int64_t new_stride,
+    const dd_paged_cache* cache, const int32_t* lengths, int B, int Hq, int max_len,
+    float softmax_scale, void* out, float* lse, const float* mass_in, float* mass_out,
+    int64_t mass_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device scratch dd_paged_attention needs (0 on invalid sizes). Pure host
+ * function; the bound holds on any device. Dominant terms: partial outputs of split
+ * sequences, and with masses the scores (B * Hq * max_len * 4 bytes). */
+size_t dd_paged_attention_workspace_size(int B, int Hq, int Hkv, int d, int max_len,
+                                         int with_mass);
+
+/*
+ * dd_cache_evict -- bring every sequence of a cache down to at most `budget` slots,
+ * dropping those of the least accumulated attention mass.
+ *   Kept: the slots whose position (pos_in) is below `sink` or among the last `recent`
+ *   (above max pos - recent), then the largest masses; equal masses: the lower slot.
+ *   (NaN ranks below every number. Should more than `budget` slots be protected, the
+ *   lowest of them are kept.)
+ * A kept slot at or beyond the new length moves into a freed slot below it: the i-th
+ * freed slot from below takes the i-th such slot. So slots are not in order of position
+ * afterwards (attention does not depend on their order, as long as keys carry their
+ * position) and only moved rows are copied. Running the call again on the same inputs
+ * gives the same result: rows that move are left where they were.
+ *
+ * cache           layers = 1; the pages below the new length must be the sequence's own
+ * lengths         [N] int32, 0 .. max_len
+ * mass_in, pos_in [N, .] fp32 / int32, row stride `stride` >= max_len
+ * mass_out, pos_out  same shapes, not the inputs' memory; slots at or beyond the new
+ *                 length are not written
+ * src_out         [N, .] int32, stride `stride`, or NULL: the old slot of each new one (to
+ *                 move whatever else a program keeps per slot)
+ * lengths_out     [N] int32 = min(lengths, budget), not the memory of `lengths`
+ * A slot in a hole moves nothing (its row stays as it is); mass and position follow.
+ * Errors: DD_ERR_INVALID_ARG for null pointers, sizes or strides out of range,
+ * budget < 1, sink or recent < 0, sink + recent > budget, outputs that are the inputs'
+ * memory; DD_ERR_UNSUPPORTED for d not in {64,128}, N > 65535 or max_len > 524288.
+ */
+dd_status dd_cache_evict(
+    const dd_paged_cache* cache, const int32_t* lengths, int N, int max_len,
+    int budget, int sink, int recent, const float* mass_in, const int32_t* pos_in,
+    int64_t stride, float* mass_out, int32_t* pos_out, int32_t* src_out,
+    int32_t* lengths_out, void* stream);
+
+/*
+ * dd_beam_select -- one step of beam search over B requests of K beams:
+ *   score(k, v) = score_in[k] + x_kv - log sum_u e^{x_ku}   for every token of a live beam,
+ *   a beam that is done (done_in) has the one candidate (k, eos) at its own score,
+ *   a beam whose score_in is -inf or NaN has none (an empty slot).
+ * The K best of the K V candidates, by score, equal scores by the lower k V + v; scores
+ * are compared in 64 bits. A logit of -inf (or NaN) is no candidate and adds nothing to
+ * the sum; +inf is not allowed. Where there are fewer than K candidates the rest get
+ * parent -1, token -1, score -inf, done 0.
+ *
+ * logits          [B,K,V], row stride ld >= V, DD_F32 or DD_BF16, 16-byte aligned,
+ *                 ld * element a multiple of 16 bytes
+ * score_in        [B,K] fp32; done_in [B,K] u8 or NULL (none); eos in [-1, V), -1: no token
+ *                 ends a beam (a done beam then stands at k V and gets token -1)
+ * parent, token   [B,K] int32; score_out [B,K] fp32 in descending order (not score_in's memory);
+ * done_out        [B,K] u8 or NULL: the parent was done, or the token is eos (not done_in's
+ *                 memory)
+ * workspace       at least dd_beam_select_workspace_size(B,K,V,dtype) bytes, 256-byte aligned;
+ *                 contents on entry are ignored; calls that share it must not overlap.
+ * Errors: DD_ERR_INVALID_ARG for null pointers, sizes, alignment, eos outside [-1, V), outputs
+ * that are the inputs' memory, a short workspace; DD_ERR_UNSUPPORTED for K > 64,
+ * V > 2^23 or B * K > 2^20.
+ */
+dd_status dd_beam_select(
+    const void* logits, dd_dtype dtype, int B, int K, int V, int64_t ld,
+    const float* score_in, const uint8_t* done_in, int eos,
+    int32_t* parent, int32_t* token, float* score_out, uint8_t* done_out,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+size_t dd_beam_select_workspace_size(int B, int K, int V, dd_dtype dtype);
+
+/* One state of dd_beam_reorder: B * K rows of row_bytes contiguous bytes each, row n
+ * at n * stride bytes. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t row_bytes;
+  int64_t src_stride;  /* bytes */
+  int64_t dst_stride;
+} dd_row_state;
+
+/*
+ * dd_beam_reorder -- states follow their parents: row b K + k of each dst is row
+ * b K + parent[b,k] of its src. A parent outside [0, K) (an empty slot) keeps its own
+ * row k. Up to 8 states in one launch; src and dst of a state must not overlap.
+ * Errors: DD_ERR_INVALID_ARG for null pointers, sizes, strides below row_bytes (either
+ * may be anything when B * K = 1), src == dst; DD_ERR_UNSUPPORTED for n_states > 8 or
+ * B * K > 2^20.
+ */
+dd_status dd_beam_reorder(const int32_t* parent, int B, int K, const dd_row_state* states,
+                          int n_states, void* stream);
+
+/*
+ * dd_paged_fork -- the paged caches of B requests of K beams follow their parents
+ * without copying what can be shared. Beam n = b K + k takes the table of its parent
+ * p = b K + parent[n] (own row for a parent outside [0, K)):
+ *   table_out[n, i] = page_table[p, i]  for every full page i < f = lengths[p] / page_size;
+ *   table_out[n, f] = fresh[n], the page the beam's next token goes to (if f < max_pages),
+ *   with the rows of page_table[p, f] that are filled copied into it, in every layer
+ *   (if that page is a hole and rows of it count, table_out[n, f] stays a hole);
+ *   lengths_out[n] = lengths[p]. Entries beyond f are not written.
+ * Full pages are thus shared and never written again. Which pages are free afterwards is
+ * the caller's bookkeeping.
+ * fresh        [B*K] int32: pages that no beam of the call uses, all different. An id
+ *              outside [0, n_pages), where it is needed, records DD_ERR_BOUNDS, and
+ *              table_out[n, f] becomes a hole.
+ * table_out    [B*K, max_pages], row stride out_stride, not page_table's memory
+ * lengths_out  [B*K], not lengths' memory
+ * Lengths beyond max_pages * page_size record DD_ERR_BOUNDS and are clamped.
+ * Errors: DD_ERR_INVALID_ARG for null pointers, sizes, strides, outputs that are the
+ * inputs' memory; DD_ERR_UNSUPPORTED for d not in {64,128} or B * K > 65535.
+ */
+dd_status dd_paged_fork(const dd_paged_cache* cache, const int32_t* parent, int B, int K,
+                        const int32_t* lengths, const int32_t* fresh, int32_t* table_out,
+                        int64_t out_stride, int32_t* lengths_out, void* stream);
+
+/* Human-readable name of a status. */
 const char* dd_status_string(dd_status s);
 
 /* Synchronises `stream`, then returns and clears the device error word

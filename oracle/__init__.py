@@ -22,10 +22,11 @@ Modules:
   vocab      per-row verifier/drafter statistics and coupled Gumbel samples
   seeds      stability score and top-k seed selection
   decide     KEEP / REPLACE / REMASK policies
+  cached     token-by-token decoding: paged attention, eviction, beam selection
 
 Parity status: every function is pinned by invariants, closed forms, brute
 force or library routines (see tests/test_oracle_*.py); the pages print no
 worked numeric example for any step, so no value-level golden from the pages
 exists.
 """
-from . import philox, attention, vocab, seeds, decide  # noqa: F401
+from . import philox, attention, vocab, seeds, decide, cached  # noqa: F401

@@ -97,6 +97,62 @@ cudaError_t launch_decide(const dd_decide_params& p, const int32_t* tokens,
                           uint8_t* decision, int32_t* new_tokens, uint8_t* accepted,
                           cudaStream_t stream);
 
+// dd_paged_attention's arguments, validated.
+struct PagedCall {
+  const void* q;
+  int64_t q_stride;
+  const void *k_new, *v_new;
+  int64_t new_stride;
+  const dd_paged_cache* cache;
+  const int32_t* lengths;
+  int B, Hq, max_len;
+  float scale;
+  void* out;
+  float* lse;
+  const float* mass_in;
+  float* mass_out;
+  int64_t mass_stride;
+  void* workspace;
+};
+cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream);
+size_t paged_attention_workspace(int B, int Hq, int Hkv, int d, int max_len, bool mass);
+// An upper bound of the tiles its plan counts in 32 bits.
+int64_t paged_attention_tiles(int B, int Hq, int max_len);
+
+struct EvictCall {
+  const dd_paged_cache* cache;
+  const int32_t* lengths;
+  int N, max_len, budget, sink, recent;
+  const float* mass_in;
+  const int32_t* pos_in;
+  int64_t stride;
+  float* mass_out;
+  int32_t *pos_out, *src_out, *lengths_out;
+};
+cudaError_t launch_cache_evict(const EvictCall& p, cudaStream_t stream);
+
+struct BeamCall {
+  const void* logits;
+  dd_dtype dtype;
+  int B, K, V;
+  int64_t ld;
+  const float* score_in;
+  const uint8_t* done_in;
+  int eos;
+  int32_t *parent, *token;
+  float* score_out;
+  uint8_t* done_out;
+  void* workspace;
+};
+cudaError_t launch_beam_select(const BeamCall& p, cudaStream_t stream);
+size_t beam_select_workspace(int B, int K, int V, dd_dtype dtype);
+
+cudaError_t launch_beam_reorder(const int32_t* parent, int B, int K, const dd_row_state* states,
+                                int n_states, cudaStream_t stream);
+cudaError_t launch_paged_fork(const dd_paged_cache& cache, const int32_t* parent, int B, int K,
+                              const int32_t* lengths, const int32_t* fresh, int32_t* table_out,
+                              int64_t out_stride, int32_t* lengths_out, cudaStream_t stream);
+
 cudaError_t launch_selftest_wait(uint32_t limit, cudaStream_t stream);
 cudaError_t launch_selftest_bounds(int n, int index, int* value, cudaStream_t stream);
 cudaError_t launch_selftest_gumbel(float* g_of_k, float* j_of_k, const float* g_req,
@@ -109,5 +165,16 @@ constexpr int kSelectMaxL = 24576;
 // flags live in shared memory).
 constexpr int kTcMaxL = 32768;
 constexpr int kSelectMaxK = 1024;
+// Most sequences of a paged-attention call (their tile counts live in shared memory) and
+// most query heads (so do their softmax statistics).
+constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxHeads = 8192;
+constexpr int kPagedMaxLen = 1 << 30;
+// Most slots of a sequence dd_cache_evict handles (one bit each, and one rank per 32, in
+// shared memory).
+constexpr int kEvictMaxLen = 524288;
+constexpr int kBeamMaxK = 64;
+constexpr int kBeamMaxV = 1 << 23;
+constexpr int kMaxRowStates = 8;
 
 }  // namespace dd

@@ -7,3 +7,7 @@
 #include "dd_attention_tc2.cu"
 #include "dd_select.cu"
 #include "dd_static.cu"
+#include "dd_paged.cu"
+#include "dd_evict.cu"
+#include "dd_beam.cu"
+#include "dd_cached_api.cu"

@@ -33,6 +33,8 @@ EXPORTED = (
     "dd_dualview_attention_workspace_size", "dd_verify_logits",
     "dd_verify_logits_workspace_size", "dd_verify_logits_static",
     "dd_coupled_gumbel", "dd_select_seeds", "dd_select_seeds_ex", "dd_decide",
+    "dd_paged_attention", "dd_paged_attention_workspace_size", "dd_cache_evict",
+    "dd_beam_select", "dd_beam_select_workspace_size", "dd_beam_reorder", "dd_paged_fork",
     "dd_status_string",
     "dd_get_device_error", "dd_set_spin_limit", "dd_selftest_bounded_wait",
     "dd_selftest_gumbel_screen", "dd_bounds_checked", "dd_selftest_bounds_check",
@@ -56,6 +58,21 @@ class _DecideParams(ctypes.Structure):
                 ("tau_conf", ctypes.c_float), ("temperature", ctypes.c_float),
                 ("tau_commit", ctypes.c_float), ("min_commit", ctypes.c_int),
                 ("seed", ctypes.c_uint64), ("step", ctypes.c_uint64)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("layers", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int)]
+
+
+class _RowState(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("src_stride", ctypes.c_int64), ("dst_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -104,6 +121,21 @@ def lib():
     L.dd_decide.argtypes = [ctypes.POINTER(_DecideParams), P, P, P, ctypes.POINTER(_RowStats),
                             I, I, I, I, P, P, P, P]
     L.dd_decide.restype = I
+    C = ctypes.POINTER(_PagedCache)
+    L.dd_paged_attention.argtypes = [P, I64, P, P, I64, C, P, I, I, I, F, P, P, P, P, I64, P, SZ, P]
+    L.dd_paged_attention.restype = I
+    L.dd_paged_attention_workspace_size.argtypes = [I] * 6
+    L.dd_paged_attention_workspace_size.restype = SZ
+    L.dd_cache_evict.argtypes = [C, P, I, I, I, I, I, P, P, I64, P, P, P, P, P]
+    L.dd_cache_evict.restype = I
+    L.dd_beam_select.argtypes = [P, I, I, I, I, I64, P, P, I, P, P, P, P, P, SZ, P]
+    L.dd_beam_select.restype = I
+    L.dd_beam_select_workspace_size.argtypes = [I] * 4
+    L.dd_beam_select_workspace_size.restype = SZ
+    L.dd_beam_reorder.argtypes = [P, I, I, ctypes.POINTER(_RowState), I, P]
+    L.dd_beam_reorder.restype = I
+    L.dd_paged_fork.argtypes = [C, P, I, I, P, P, P, I64, P, P]
+    L.dd_paged_fork.restype = I
     L.dd_status_string.argtypes = [I]
     L.dd_status_string.restype = ctypes.c_char_p
     L.dd_get_device_error.argtypes = [P]
@@ -329,6 +361,289 @@ def dd_decide(policy, tokens, is_seed, eligible, stats: RowStats, pos_offset, de
                          ctypes.byref(stats._c()), B, L, R, int(pos_offset), _ptr(decision),
                          _ptr(new_tokens), _ptr(accepted), _stream(stream))
     _check("dd_decide", st)
+
+
+# ------------------------------------------------------------------ cached decoding
+# Every tensor of a call is checked here -- device, type, shape, layout -- before its
+# address reaches the library; the call runs on that device, on `stream` (None: its
+# current stream), and a workspace that is not given is allocated for that stream.
+def _dev(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"libdd takes device memory: {name} is on the CPU")
+    return t.device
+
+
+def _arg(t, name, dtype, shape, device, packed=True):
+    """Address of a tensor of the given type, shape and device. packed: contiguous;
+    otherwise only rows (all dimensions but the first) must be."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not (t.is_contiguous() if packed or t.shape[0] < 2 else t[0].is_contiguous()):
+        raise ValueError(f"{name} must be contiguous" + ("" if packed else " within a row"))
+    return t.data_ptr()
+
+
+def _opt(t, *args, **kw):
+    return None if t is None else _arg(t, *args, **kw)
+
+
+def _row_stride(t):
+    """Elements from row to row (0 where there is one row)."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+class _On:
+    """Makes `device` current for a call (a change of device only where one is needed)."""
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _scratch(nbytes, device, stream):
+    """Device scratch that the allocator reuses in the order of `stream`."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    if workspace is None:
+        return _scratch(nbytes, device, stream)
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+class PagedCache:
+    """A paged K/V cache: k, v [pages, page_size, Hkv, d] or, for several layers that share
+    page ids, [layers, pages, page_size, Hkv, d], and page_table [N, max_pages] int32.
+    k and v have the same shape and strides, any strides with a unit last one (so a pool
+    stored heads first is passed as its transposed view). A page id below 0 is a hole."""
+
+    def __init__(self, k, v, page_table):
+        dev = _dev(k, "k")
+        if _dev(v, "v") != dev or _dev(page_table, "page_table") != dev:
+            raise ValueError("k, v and page_table must be on one device")
+        if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("k and v must be [pages, page_size, Hkv, d] or [layers, pages, "
+                             "page_size, Hkv, d], of the same shape and strides")
+        if v.dtype != k.dtype:
+            raise ValueError("k and v must have the same dtype")
+        if k.numel() == 0:
+            raise ValueError("k and v must not be empty")
+        if k.stride(-1) != 1:
+            raise ValueError("k and v must have a unit stride over d")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.numel() == 0:
+            raise ValueError("page_table must be a non-empty [N, max_pages] int32 tensor")
+        if page_table.stride(1) != 1 and page_table.shape[1] > 1:
+            raise ValueError("page_table must be contiguous within a row")
+        self.k, self.v, self.page_table, self.device, self.dtype = k, v, page_table, dev, k.dtype
+        *layers, self.n_pages, self.page_size, self.Hkv, self.d = k.shape
+        self.layers = layers[0] if layers else 1
+        self.N, self.max_pages = page_table.shape
+        s = [st if n > 1 else 0 for n, st in zip(k.shape, k.stride())]
+        self._c = _PagedCache(k.data_ptr(), v.data_ptr(), s[0] if layers else 0, *s[-4:-1],
+                              self.layers, self.n_pages, self.page_size, self.Hkv, self.d,
+                              _dtype_code(k), page_table.data_ptr(),
+                              page_table.stride(0) if self.N > 1 else self.max_pages, self.max_pages)
+
+    @property
+    def slots(self):
+        """Slots a table row has room for."""
+        return self.max_pages * self.page_size
+
+    def layer(self, i):
+        """One layer's cache of a several-layer one (the same memory and page table)."""
+        if self.k.dim() != 5:
+            raise ValueError("the cache has a single layer")
+        return PagedCache(self.k[i], self.v[i], self.page_table)
+
+    def with_table(self, page_table):
+        """The same pools under another page table (dd_paged_fork's, say)."""
+        return PagedCache(self.k, self.v, page_table)
+
+    def _sequences(self, n):
+        if n != self.N:
+            raise ValueError(f"the page table has {self.N} rows, the call {n} sequences")
+
+    def _ref(self):
+        return ctypes.byref(self._c)
+
+
+def dd_paged_attention_workspace_size(B, Hq, Hkv, d, max_len, with_mass=False) -> int:
+    return int(lib().dd_paged_attention_workspace_size(B, Hq, Hkv, d, max_len, int(bool(with_mass))))
+
+
+def dd_paged_attention(q, cache: PagedCache, lengths, out, lse=None, k_new=None, v_new=None,
+                       mass=None, mass_out=None, max_len=None, workspace=None, softmax_scale=0.0,
+                       stream=None):
+    """Attention of one new token per sequence over a paged cache. q [B,Hq,d] (its rows may
+    be a slice of wider ones); lengths [B] int32; out [B,Hq,d]; lse [B,Hq] fp32;
+    k_new, v_new [B,Hkv,d]: appended at slot lengths - 1 first; mass (None: zero),
+    mass_out [B,M] fp32 with M >= max_len: the attention mass per slot, added up. max_len:
+    bound on lengths (None: the smaller of M and what the page table has room for)."""
+    dev = _dev(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    cache._sequences(B)
+    if d != cache.d or Hq % cache.Hkv:
+        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.Hkv} heads of {cache.d}")
+    if cache.device != dev:
+        raise ValueError(f"q is on {dev}, the cache on {cache.device}")
+    if max_len is None:
+        max_len = cache.slots if mass_out is None else min(cache.slots, mass_out.shape[-1])
+    new = (B, cache.Hkv, d)
+    f32 = torch.float32
+    if mass_out is None and mass is not None:
+        raise ValueError("mass without mass_out")
+    rows = None if mass_out is None else (B, mass_out.shape[-1])
+    if mass is not None and mass.stride() != mass_out.stride():
+        raise ValueError("mass and mass_out must have the same strides")
+    qp = _arg(q, "q", cache.dtype, (B, Hq, d), dev, packed=False)
+    kp, vp = (_opt(t, n, cache.dtype, new, dev, packed=False)
+              for t, n in ((k_new, "k_new"), (v_new, "v_new")))
+    if k_new is not None and v_new is not None and _row_stride(k_new) != _row_stride(v_new):
+        raise ValueError("k_new and v_new must have the same strides")
+    op = _arg(out, "out", cache.dtype, (B, Hq, d), dev)
+    args = (_arg(lengths, "lengths", torch.int32, (B,), dev),)
+    lp = _opt(lse, "lse", f32, (B, Hq), dev)
+    mi = _opt(mass, "mass", f32, rows, dev, packed=False)
+    mo = _opt(mass_out, "mass_out", f32, rows, dev, packed=False)
+    stride = 0 if mass_out is None else mass_out.stride(0) if B > 1 else mass_out.shape[1]
+    with _On(dev):
+        ws = _workspace(workspace, 0 if workspace is not None else dd_paged_attention_workspace_size(
+            B, Hq, cache.Hkv, d, int(max_len), mass_out is not None), dev, stream)
+        st = lib().dd_paged_attention(
+            qp, _row_stride(q), kp, vp, 0 if k_new is None else _row_stride(k_new), cache._ref(),
+            *args, B, Hq, int(max_len), float(softmax_scale), op, lp, mi, mo, stride,
+            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    _check("dd_paged_attention", st)
+
+
+def dd_cache_evict(cache: PagedCache, lengths, mass, pos, budget, mass_out, pos_out, lengths_out,
+                   sink=0, recent=0, src=None, max_len=None, stream=None):
+    """Bring every sequence down to `budget` slots by accumulated mass. mass, mass_out
+    [N,M] fp32, pos, pos_out, src (optional output: each new slot's old one) [N,M] int32,
+    M >= max_len; lengths, lengths_out [N] int32; outputs are other tensors than inputs.
+    max_len: bound on lengths (None: the smaller of M and what the page table has room for)."""
+    dev = _dev(mass, "mass")
+    if mass.dim() != 2:
+        raise ValueError("mass must be [N, M]")
+    N, M = mass.shape
+    cache._sequences(N)
+    if cache.device != dev:
+        raise ValueError(f"mass is on {dev}, the cache on {cache.device}")
+    max_len = min(M, cache.slots) if max_len is None else int(max_len)
+    i32, f32 = torch.int32, torch.float32
+    ptr = [_arg(t, n, dt, (N, M), dev) for t, n, dt in
+           ((mass, "mass", f32), (pos, "pos", i32), (mass_out, "mass_out", f32),
+            (pos_out, "pos_out", i32))]
+    sp = _opt(src, "src", i32, (N, M), dev)
+    ln, lo = (_arg(t, n, i32, (N,), dev) for t, n in ((lengths, "lengths"), (lengths_out, "lengths_out")))
+    with _On(dev):
+        st = lib().dd_cache_evict(cache._ref(), ln, N, max_len, int(budget), int(sink), int(recent),
+                                  ptr[0], ptr[1], M, ptr[2], ptr[3], sp, lo, _stream(stream))
+    _check("dd_cache_evict", st)
+
+
+def dd_beam_select_workspace_size(B, K, V, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else _dtype_code(torch.empty(0, dtype=dtype))
+    return int(lib().dd_beam_select_workspace_size(B, K, V, code))
+
+
+def dd_beam_select(logits, score, parent, token, score_out, done=None, done_out=None, eos=-1,
+                   workspace=None, stream=None):
+    """One step of beam search: logits [B,K,V] (a view narrowed from a wider [B,K,ld] buffer is
+    accepted), score, score_out [B,K] fp32, parent, token [B,K] int32, done, done_out [B,K]
+    uint8. Outputs are other tensors than inputs."""
+    dev = _dev(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, K, V]")
+    B, K, V = logits.shape
+    ld = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else -(-V // 8) * 8
+    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != K * ld):
+        raise ValueError("logits must be [B,K,V] with unit vocabulary stride and packed rows")
+    i32, f32, bk = torch.int32, torch.float32, (B, K)
+    sp, so = (_arg(t, n, f32, bk, dev) for t, n in ((score, "score"), (score_out, "score_out")))
+    pp, tp = (_arg(t, n, i32, bk, dev) for t, n in ((parent, "parent"), (token, "token")))
+    dp, do = (_opt(t, n, torch.uint8, bk, dev) for t, n in ((done, "done"), (done_out, "done_out")))
+    code = _dtype_code(logits)
+    with _On(dev):
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        lib().dd_beam_select_workspace_size(B, K, V, code), dev, stream)
+        st = lib().dd_beam_select(logits.data_ptr(), code, B, K, V, ld, sp, dp, int(eos), pp, tp, so,
+                                  do, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    _check("dd_beam_select", st)
+
+
+def dd_beam_reorder(parent, states, stream=None):
+    """States follow their parents: parent [B,K] int32; states: up to 8 pairs (src, dst) of
+    tensors [B*K, ...] or [B,K,...], contiguous, of the same shape and dtype."""
+    dev = _dev(parent, "parent")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, K]")
+    B, K = parent.shape
+    n = B * K
+    c = (_RowState * max(1, len(states)))()
+    for i, (src, dst) in enumerate(states):
+        sp = _arg(src, "src", src.dtype, src.shape, dev)
+        dp = _arg(dst, "dst", src.dtype, src.shape, dev)
+        if src.shape[0] != n and src.shape[:2] != (B, K):
+            raise ValueError(f"a state must be [B*K, ...] or [B, K, ...], got {tuple(src.shape)}")
+        size = src.numel() * src.element_size()
+        row = size // n
+        if sp < dp + size and dp < sp + size:
+            raise ValueError("src and dst of a state must not overlap")
+        c[i] = _RowState(sp, dp, row, row, row)
+    pp = _arg(parent, "parent", torch.int32, (B, K), dev)
+    with _On(dev):
+        st = lib().dd_beam_reorder(pp, B, K, c, len(states), _stream(stream))
+    _check("dd_beam_reorder", st)
+
+
+def dd_paged_fork(cache: PagedCache, parent, lengths, fresh, table_out, lengths_out, stream=None):
+    """The beams' caches follow their parents: parent [B,K] int32; lengths, fresh, lengths_out
+    [B*K] int32; table_out [B*K, max_pages] int32. Full pages are shared; page fresh[n], with
+    the filled rows of a partly filled last page, is where beam n goes on. Outputs are other
+    tensors than inputs."""
+    dev = _dev(parent, "parent")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, K]")
+    B, K = parent.shape
+    n = B * K
+    cache._sequences(n)
+    if cache.device != dev:
+        raise ValueError(f"parent is on {dev}, the cache on {cache.device}")
+    i32 = torch.int32
+    pp = _arg(parent, "parent", i32, (B, K), dev)
+    lp, fp, lo = (_arg(t, name, i32, (n,), dev) for t, name in
+                  ((lengths, "lengths"), (fresh, "fresh"), (lengths_out, "lengths_out")))
+    to = _arg(table_out, "table_out", i32, (n, cache.max_pages), dev, packed=False)
+    with _On(dev):
+        st = lib().dd_paged_fork(cache._ref(), pp, B, K, lp, fp, to,
+                                 table_out.stride(0) if n > 1 else cache.max_pages, lo, _stream(stream))
+    _check("dd_paged_fork", st)
 
 
 def dd_get_device_error(stream=None) -> int:

@@ -1,0 +1,212 @@
+"""dd_beam_select, dd_beam_reorder and dd_paged_fork against the oracle.
+
+Candidates are compared exactly. Scores of different beams can lie closer than the sums'
+rounding: a log-sum of V fp32 exponentials is off by less than 2^-22 + V 2^-24 relative at
+the very worst and, with errors of either sign, by about 2^-22; cases whose best K + 1
+candidates of different beams lie within 4e-6 would be skipped, and none of these seeds has
+one (asserted)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cached as OC
+from speculative_verification_cover_b200 import dd
+
+pytestmark = pytest.mark.gpu
+GAP = 4e-6
+
+
+def _select(logits, score, done=None, eos=-1, **kw):
+    B, K, V = logits.shape
+    i = dict(dtype=torch.int32, device="cuda")
+    parent, token = torch.full((B, K), -9, **i), torch.full((B, K), -9, **i)
+    out = torch.full((B, K), 7.0, device="cuda")
+    done_out = torch.full((B, K), 9, dtype=torch.uint8, device="cuda")
+    dd.dd_beam_select(logits, score, parent, token, out, done=done, done_out=done_out, eos=eos, **kw)
+    torch.cuda.synchronize()
+    assert dd.dd_get_device_error() == dd.DD_OK
+    return parent.cpu().numpy(), token.cpu().numpy(), out.cpu().numpy(), done_out.cpu().numpy()
+
+
+def _check(logits, score, done=None, eos=-1, gaps=True):
+    got = _select(logits, score, done, eos)
+    x = logits.float().cpu().numpy()
+    B, K, V = x.shape
+    for b in range(B):
+        dn = None if done is None else done[b].cpu().numpy()
+        if gaps:
+            best = OC.beam_candidates(x[b], score[b].cpu().numpy(), dn, eos, V)[:K + 1]
+            for (s, i), (s2, i2) in zip(best, best[1:]):
+                assert i // V == i2 // V or s2 - s > GAP
+        parent, token, out, ended = OC.beam_select(x[b], score[b].cpu().numpy(), dn, eos)
+        assert got[0][b].tolist() == parent.tolist(), b
+        assert got[1][b].tolist() == token.tolist(), b
+        assert got[3][b].tolist() == ended.tolist(), b
+        fin = np.isfinite(out)
+        assert np.array_equal(np.isneginf(got[2][b]), ~fin)
+        # half a step of the value, and the log-sum's error
+        assert np.all(np.abs(got[2][b][fin] - out[fin]) <= 2.0 ** -24 * np.abs(out[fin]) + 1e-6)
+    return got
+
+
+def _logits(seed, B, K, V, dtype, pad=0, std=3.0):
+    gen = torch.Generator().manual_seed(seed)
+    ld = -(-(V + pad) // 8) * 8
+    x = (torch.randn(B, K, ld, generator=gen) * std).to(dtype)
+    x[..., V:] = float("inf")  # columns behind the vocabulary are not candidates
+    score = -torch.rand(B, K, generator=gen) * 4 - 10
+    return x.cuda()[..., :V], score.cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,K,V", [(1, 1, 1), (1, 4, 3), (2, 3, 7), (3, 1, 4097), (2, 5, 1000), (1, 64, 63),
+                                   (2, 64, 9000), (4, 8, 32003), (1, 16, 126464), (2, 33, 8193)])
+def test_shapes(dtype, B, K, V):
+    x, score = _logits(1, B, K, V, dtype, pad=8)
+    gen = torch.Generator().manual_seed(2)
+    done = (torch.rand(B, K, generator=gen) < 0.2).to(torch.uint8).cuda()
+    _check(x, score)
+    _check(x, score, done, eos=V // 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_ties_go_to_the_lowest_index(dtype):
+    # equal logits in a beam: by index; equal beams: by beam
+    for K, V in ((4, 10), (8, 20000), (64, 9000)):
+        x = torch.zeros(2, K, -(-V // 8) * 8, dtype=dtype, device="cuda")[..., :V]
+        _check(x, torch.zeros(2, K, device="cuda"), gaps=False)
+        _check(x, torch.arange(2 * K, device="cuda").view(2, K).float(), gaps=False)
+    x, _ = _logits(3, 1, 6, 5000, dtype)
+    x = x[:, :1].round().expand(1, 6, 5000)
+    wide = torch.empty(1, 6, 5000, dtype=dtype, device="cuda").copy_(x)
+    _check(wide, torch.zeros(1, 6, device="cuda"), gaps=False)
+    two = wide.clone()
+    two[..., ::2] = -0.0
+    two[..., 1::2] = 0.0
+    _check(two, torch.zeros(1, 6, device="cuda"), gaps=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_one_thread_and_one_beam_hold_all_the_best(dtype):
+    # every large logit within one vector's stride of threads; one beam far ahead
+    x, score = _logits(4, 1, 64, 30000, dtype, std=1.0)
+    x[0, :, 4096:4096 + 64] = torch.arange(64, device="cuda").to(dtype) + 20
+    _check(x, score)
+    score[0, 17] = 0.0
+    _check(x, score)
+    for stride in (256 * 8, 256 * 4):
+        x[0, 17, 5::stride] = 60.0 + torch.arange(x[0, 17, 5::stride].numel(), device="cuda").to(dtype)
+        _check(x, score)
+
+
+def test_banned_and_empty():
+    inf, nan = float("inf"), float("nan")
+    x, score = _logits(5, 2, 4, 100, torch.float32, pad=4)
+    x[0, 0] = -inf                     # a beam without candidates
+    x[0, 1, 3:] = -inf                 # three tokens left
+    x[0, 2, ::2] = nan
+    x[1] = -inf                        # a request without candidates
+    _check(x, score)
+    score[0, 3] = -inf                 # an empty slot
+    score[0, 2] = nan
+    _check(x, score)
+    done = torch.zeros(2, 4, dtype=torch.uint8, device="cuda")
+    done[1, 2] = done[0, 3] = 1
+    _check(x, score, done, eos=0)
+    _check(x, score, done, eos=-1)
+    done.fill_(1)
+    _check(x, score, done, eos=99)
+
+
+def test_first_step_starts_from_one_beam():
+    x, _ = _logits(6, 3, 8, 5000, torch.bfloat16)
+    score = torch.full((3, 8), float("-inf"), device="cuda")
+    score[:, 0] = 0.0
+    got = _check(x, score)
+    assert np.all(got[0] == 0)
+
+
+def test_other_stream_and_graph():
+    x, score = _logits(7, 4, 8, 20000, torch.bfloat16)
+    want = _select(x, score)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = _select(x, score, stream=side)
+    for a, b in zip(want, got):
+        assert np.array_equal(a, b)
+    i = dict(dtype=torch.int32, device="cuda")
+    parent, token, out = torch.zeros(4, 8, **i), torch.zeros(4, 8, **i), torch.zeros(4, 8, device="cuda")
+    ws = torch.empty(dd.dd_beam_select_workspace_size(4, 8, 20000, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    call = lambda: dd.dd_beam_select(x, score, parent, token, out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    y, s2 = _logits(8, 4, 8, 20000, torch.bfloat16)
+    x.copy_(y)
+    score.copy_(s2)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = _select(y, s2)
+    assert np.array_equal(parent.cpu().numpy(), want[0]) and np.array_equal(token.cpu().numpy(), want[1])
+
+
+@pytest.mark.parametrize("shape,dtype", [((1,), torch.uint8), ((7,), torch.uint8), ((3,), torch.int32),
+                                         ((5, 4), torch.float32), ((129, 257), torch.bfloat16),
+                                         ((100000,), torch.int32)])
+def test_reorder(shape, dtype):
+    B, K = 3, 5
+    gen = torch.Generator().manual_seed(9)
+    parent = torch.randint(-1, K + 1, (B, K), generator=gen).to(torch.int32)
+    states = [torch.randint(0, 100, (B, K, *shape), generator=gen).to(dtype).cuda(),
+              torch.randint(0, 100, (B * K, *shape), generator=gen).to(dtype).cuda()]
+    outs = [torch.full_like(s, 101) for s in states]
+    dd.dd_beam_reorder(parent.cuda(), list(zip(states, outs)))
+    rows = torch.tensor(OC.parents(parent.numpy(), K)).cuda()
+    for s, o in zip(states, outs):
+        assert torch.equal(o.view(B * K, -1), s.view(B * K, -1)[rows])
+
+
+@pytest.mark.parametrize("layers,page,Hkv,d,dtype", [(1, 16, 8, 128, torch.bfloat16), (3, 5, 1, 64, torch.float32),
+                                                     (2, 1, 2, 64, torch.bfloat16), (1, 128, 4, 128, torch.float32)])
+def test_fork(layers, page, Hkv, d, dtype):
+    B, K = 3, 4
+    N = B * K
+    rng = np.random.default_rng(10)
+    width = 4
+    cap = width * page
+    lengths = rng.integers(0, cap + 1, N)
+    lengths[:4] = [0, page, cap, min(cap, page + 1)]
+    pages = N * width + N + 3
+    ids = rng.permutation(pages)
+    table = ids[:N * width].reshape(N, width).copy()
+    table[5, :] = -1                                   # holes stay holes
+    fresh = ids[N * width:N * width + N]
+    parent = rng.integers(-1, K, (B, K))
+    k, v = (torch.randn(layers, pages, page, Hkv, d).to(dtype) for _ in range(2))
+    kw, vw, tw = k.float().numpy().copy(), v.float().numpy().copy(), np.full((N, width), -7)
+    lw = OC.fork(parent, K, table, lengths, fresh, kw, vw, tw)
+    t = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+    kg, vg, out, lout = k.cuda(), v.cuda(), t(np.full((N, width), -7)), t(np.zeros(N))
+    dd.dd_paged_fork(dd.PagedCache(kg, vg, t(table)), t(parent), t(lengths), t(fresh), out, lout)
+    torch.cuda.synchronize()
+    assert dd.dd_get_device_error() == dd.DD_OK
+    assert np.array_equal(out.cpu().numpy(), tw) and np.array_equal(lout.cpu().numpy(), lw)
+    assert np.array_equal(kg.float().cpu().numpy(), kw) and np.array_equal(vg.float().cpu().numpy(), vw)
+
+
+def test_fork_records_bad_pages_and_lengths():
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    k = torch.randn(6, 4, 1, 64, device="cuda")
+    v = torch.randn_like(k)
+    k0 = k.clone()
+    table, out, lout = t([[0, 1], [2, 3]]), t([[-7, -7], [-7, -7]]), t([0, 0])
+    cache = dd.PagedCache(k, v, table)
+    dd.dd_paged_fork(cache, t([[1, 0]]), t([5, 6]), t([6, -1]), out, lout)  # both fresh pages are bad
+    assert dd.dd_get_device_error() == dd.DD_ERR_BOUNDS
+    assert torch.equal(k, k0) and out.tolist() == [[2, -1], [0, -1]] and lout.tolist() == [6, 5]
+    dd.dd_paged_fork(cache, t([[0, 1]]), t([100, -3]), t([4, 5]), out, lout)
+    assert dd.dd_get_device_error() == dd.DD_ERR_BOUNDS
+    assert torch.equal(k, k0) and out.tolist() == [[0, 1], [5, -1]] and lout.tolist() == [8, 0]
