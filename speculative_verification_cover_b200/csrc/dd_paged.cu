@@ -15,6 +15,7 @@
 //
 // Bound: HBM, 2 Hkv d elements per slot read once.
 #include "dd_paged.cuh"
+#include "dd_tc.cuh"
 
 namespace dd {
 
@@ -321,6 +322,348 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ tensor-core form (bf16)
+// Per warp and tile: 16 slots. S^T [16 slots x heads] = K Q^T and O^T [d x heads] += V^T P^T
+// as m16n8k16 products whose 16-row operand is the cache (8 heads, or 16 in two column
+// tiles, are the narrow side: as the 16-row operand they would waste half of it, and twice
+// the instructions). The call is bound by reading K and V, about 23 bytes a cycle and SM,
+// which leaves these instructions an idle pipe: a 128-row tcgen05 tile would wait for 128
+// slots before its first product, where a warp's 16 slots start as they arrive.
+// P is carried as two bf16 terms (16 bits of a weight), so the output has fp32 weights'
+// accuracy; one term alone would add as much error again as the output's own rounding.
+// Each warp streams its own slots through a ring of stages in shared memory (cp.async,
+// rows swizzled by 16-byte chunks) that runs on across tiles and sequences; page ids are
+// fetched one tile ahead of the copies that need them. Warps meet only to join a
+// sequence-head's results.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A place in the tile space: tile `tile` of (sequence b, pair = kv head and head block).
+struct Cursor {
+  int b, len, tiles, pair, tile;
+  __device__ __forceinline__ void enter(const PagedArgs& a, const int32_t* prefix, int at) {
+    b = at;
+    len = checked_length(a.lengths, b, a.max_len);
+    tiles = (len + kTile - 1) / kTile;
+  }
+  __device__ __forceinline__ void seek(const PagedArgs& a, const int32_t* prefix, int u) {
+    enter(a, prefix, find_sequence(prefix, a.B, u));
+    const int rel = u - prefix[b];
+    pair = rel / tiles;
+    tile = rel - pair * tiles;
+  }
+  // The next tile; u is its index, below the total.
+  __device__ __forceinline__ void next(const PagedArgs& a, const int32_t* prefix, int u) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++pair < a.c.Hkv * a.blocks) return;
+    pair = 0;
+    int n = b + 1;
+    while (prefix[n + 1] <= u) ++n;  // sequences without slots
+    enter(a, prefix, n);
+  }
+};
+
+constexpr int kWarpSlots = 16;  // slots of a tile per warp
+
+template <int D, int NT>
+struct MmaCfg {
+  static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;  // two CTAs per SM
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kHalf = kWarpSlots * kRowBytes;  // K, or V, of one stage
+  static constexpr int kRing = kPagedWarps * kStages * 2 * kHalf;
+  static constexpr int kJoin = kPagedWarps * NT * 8 * (D + 4) * 4;
+  static constexpr int kSmem = kRing + kJoin;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kPagedThreads, 2)
+paged_mma_kernel(const __grid_constant__ PagedArgs a) {
+  using C = MmaCfg<D, NT>;
+  constexpr int H = NT * 8;       // heads, padded
+  constexpr int KS = D / 16;      // k-steps of S, row tiles of O
+  constexpr int CH = D / 8;       // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;    // rows a warp copies per instruction
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int warp_tmp[kPagedWarps];
+  __shared__ float s_m[kPagedWarps][H], s_l[kPagedWarps][H];
+  float* s_o = reinterpret_cast<float*>(smem + C::kRing);  // [warp][head][D + 4]
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = plan_tiles(a, prefix, warp_tmp);
+  write_empty_rows<__nv_bfloat16>(a, prefix, D);
+  const int u0 = blockIdx.x * share, u_end = min(prefix[a.B], u0 + share);
+  if (u0 >= u_end) return;
+  const uint32_t ring = smem_u32(smem) + warp * (C::kStages * 2 * C::kHalf);
+
+  // ---- copies: the page id of this lane's slot one tile ahead, then the rows
+  Cursor lc;  // the tile whose page ids are held
+  lc.seek(a, prefix, u0);
+  int lu = u0;
+  int id = -1;
+  const auto fetch_id = [&]() {
+    const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
+    id = j < lc.len ? a.c.table[(int64_t)lc.b * a.c.table_stride + div_fast(a.c.page, j)] : -1;
+  };
+  fetch_id();
+  uint64_t held_q = 0;  // 16 bits per stage: slots that count
+  const auto issue = [&](int stage) {
+    if (lu < u_end) {
+      const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
+      const int kvh = lc.pair / a.blocks, blk = lc.pair - kvh * a.blocks;
+      const int page = checked_page(id, a.c.n_pages);
+      const bool ok = page >= 0;  // j < len is in the id
+      int64_t off = 0;
+      if (ok)
+        off = (int64_t)page * a.c.page_bytes + (int64_t)kvh * a.c.head_bytes +
+              (int64_t)(j - div_fast(a.c.page, j) * a.c.page.n) * a.c.token_bytes;
+      const uint32_t held = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      const uint32_t fresh = __ballot_sync(0xffffffffu, ok && a.k_new && j == lc.len - 1) & 0xffffu;
+      held_q = (held_q & ~(0xffffull << (16 * stage))) | ((uint64_t)held << (16 * stage));
+      const uint32_t dst = ring + stage * 2 * C::kHalf;
+      const int c = lane % CH;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const char* base = kv ? a.c.v : a.c.k;
+#pragma unroll
+        for (int i = 0; i < kWarpSlots / RPI; ++i) {
+          const int r = i * RPI + lane / CH;
+          const int64_t o = __shfl_sync(0xffffffffu, off, r);
+          const uint32_t to = dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4);
+          if (!((fresh >> r) & 1u)) cp_async16(to, base + o + c * 16, (held >> r) & 1u ? 16 : 0);
+        }
+        if (kv == 0) cp_async_commit();
+      }
+      if (fresh) {  // the new token: read from the caller, kept in the cache
+        const int r = __ffs(fresh) - 1;
+        const int64_t o = __shfl_sync(0xffffffffu, off, r);
+        for (int x = lane; x < 2 * CH; x += 32) {
+          const int kv = x / CH, cc = x - kv * CH;
+          const char* src = (kv ? a.v_new : a.k_new) + (int64_t)lc.b * a.new_bytes + kvh * C::kRowBytes + cc * 16;
+          const uint4 w = *reinterpret_cast<const uint4*>(src);
+          const uint32_t to = dst + kv * C::kHalf + r * C::kRowBytes + ((cc ^ (r & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+          if (blk == 0) *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + o + cc * 16) = w;
+        }
+      }
+      cp_async_commit();
+      if (++lu < u_end) {
+        lc.next(a, prefix, lu);
+        fetch_id();
+      }
+    } else {  // empty groups keep the count
+      cp_async_commit();
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) issue(s);
+
+  // ---- the products
+  Cursor cc;
+  cc.seek(a, prefix, u0);
+  int stage = 0;
+  for (int u = u0; u < u_end;) {
+    const int b = cc.b, len = cc.len, tiles = cc.tiles, tile0 = cc.tile;
+    const int n_tiles = min(tiles - tile0, u_end - u);
+    const int kvh = cc.pair / a.blocks, blk = cc.pair - kvh * a.blocks;
+    const int h0 = kvh * a.G + blk * a.heads;
+    const int nh = min(a.heads, a.G - blk * a.heads);
+    uint32_t q[NT][KS][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int h = t * 8 + (lane >> 2);
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(
+          a.q + (int64_t)b * a.q_bytes + (int64_t)(h0 + min(h, nh - 1)) * C::kRowBytes) + (lane & 3);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        q[t][k][0] = h < nh ? qp[k * 8] : 0u;
+        q[t][k][1] = h < nh ? qp[k * 8 + 4] : 0u;
+      }
+    }
+    float o[KS][NT][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][t][e] = 0.f;
+    }
+    for (int i = 0; i < n_tiles; ++i) {
+      __syncwarp();  // every lane has read the stage that is filled next
+      issue(stage == 0 ? C::kStages - 1 : stage - 1);
+      const uint32_t kb = ring + stage * 2 * C::kHalf, vb = kb + C::kHalf;
+      const uint32_t held = (uint32_t)(held_q >> (16 * stage)) & 0xffffu;
+      cp_async_wait<2 * C::kStages - 1>();
+      __syncwarp();
+      float s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      const int kr = lane & 15;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t f[4];
+        ldsm4(kb + kr * C::kRowBytes + (((2 * k + (lane >> 4)) ^ (kr & 7)) << 4), f);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma16816(s[t], f, q[t][k][0], q[t][k][1]);
+      }
+      // rows lane / 4 and + 8; heads 2 (lane % 4) and + 1
+      const bool in0 = (held >> (lane >> 2)) & 1u, in1 = (held >> ((lane >> 2) + 8)) & 1u;
+      uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = (e < 2 ? in0 : in1) ? s[t][e] * a.scale2 : -INFINITY;
+        if (a.scores) {
+          const int j = (tile0 + i) * kTile + warp * kWarpSlots + (lane >> 2);
+          const int g = t * 8 + 2 * (lane & 3);
+          float* sp = a.scores + (((int64_t)b * a.c.Hkv + kvh) * a.max_len + j) * a.G + blk * a.heads + g;
+          if (j < len) {
+            if (g < nh) sp[0] = s[t][0];
+            if (g + 1 < nh) sp[1] = s[t][1];
+          }
+          if (j + 8 < len) {
+            if (g < nh) sp[8 * (int64_t)a.G] = s[t][2];
+            if (g + 1 < nh) sp[8 * (int64_t)a.G + 1] = s[t][3];
+          }
+        }
+        float mx[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+          const float mn = fmaxf(m[t][e], mx[e]);
+          const float base = mn == -INFINITY ? 0.f : mn;
+          const float alpha = exp2f(m[t][e] - base);
+          m[t][e] = mn;
+          p[e] = exp2f(s[t][e] - base);
+          p[e + 2] = exp2f(s[t][e + 2] - base);
+          l[t][e] = fmaf(l[t][e], alpha, p[e] + p[e + 2]);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[k][t][e] *= alpha;
+            o[k][t][e + 2] *= alpha;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t hi = tc::pack_bf16(p[2 * r], p[2 * r + 1]);
+          const uint32_t lo = tc::pack_bf16(p[2 * r] - bf16lo(hi), p[2 * r + 1] - bf16hi(hi));
+          ph[t][r] = transpose8x8(hi);
+          pl[t][r] = transpose8x8(lo);
+        }
+      }
+      cp_async_wait<2 * C::kStages - 2>();
+      __syncwarp();
+      const int vr = (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t f[4];
+        ldsm4_trans(vb + vr * C::kRowBytes + (((2 * k + ((lane >> 3) & 1)) ^ (vr & 7)) << 4), f);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mma16816(o[k][t], f, ph[t][0], ph[t][1]);
+          mma16816(o[k][t], f, pl[t][0], pl[t][1]);
+        }
+      }
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+    }
+    // ---- join the four warps
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[t][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        l[t][e] = x;
+      }
+    __syncthreads();  // the previous piece's reads are over
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int g = t * 8 + 2 * (lane & 3) + e;
+        if (lane < 4) {
+          s_m[warp][g] = m[t][e];
+          s_l[warp][g] = l[t][e];
+        }
+        float* op = s_o + (warp * H + g) * (D + 4) + (lane >> 2);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          op[k * 16] = o[k][t][e];
+          op[k * 16 + 8] = o[k][t][e + 2];
+        }
+      }
+    __syncthreads();
+    const bool starts = tile0 == 0, whole = starts && n_tiles == tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
+    for (int i = threadIdx.x; i < nh * (D / 4); i += kPagedThreads) {
+      const int g = i / (D / 4), e = (i - g * (D / 4)) * 4;
+      float mm = s_m[0][g];
+#pragma unroll
+      for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kPagedWarps; ++w) {
+        const float f = exp2f(s_m[w][g] - base);
+        ll = fmaf(s_l[w][g], f, ll);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * H + g) * (D + 4) + e);
+        oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
+        oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
+      }
+      if (whole) {
+        const int64_t h = (int64_t)b * a.Hq + h0 + g;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
+        *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
+        if (e == 0) {
+          const float z2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+          a.lse2[h] = z2;
+          if (a.lse) a.lse[h] = z2 * kLn2;
+        }
+      } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
+        *reinterpret_cast<float4*>(a.part_o + (slot * a.heads + g) * D + e) = oo;
+        if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
+      }
+    }
+    u += n_tiles;
+    if (u < u_end) {
+      cc.tile = tile0 + n_tiles - 1;
+      cc.next(a, prefix, u);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ join and masses
 // CTAs whose tiles hold a sequence-head: first and last, from the plan of the main kernel.
 struct Span {
@@ -473,9 +816,24 @@ cudaError_t launch_simt(const PagedArgs& a, size_t smem, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-int heads_per_block(int G) {
-  const int blocks = head_blocks(G, 8);
+// bf16: up to 16 heads in one pass over the cache (two column tiles); fp32: 8.
+int heads_per_block(int G, bool bf16) {
+  const int blocks = head_blocks(G, bf16 ? kMaxHeads : 8);
   return (G + blocks - 1) / blocks;
+}
+
+template <int D, int NT>
+cudaError_t launch_mma(const PagedArgs& a, size_t smem, cudaStream_t stream) {
+  static thread_local int configured_for = -1;
+  const int bytes = MmaCfg<D, NT>::kSmem + (int)smem;
+  if (configured_for != device_info().device) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               MmaCfg<D, NT>::kSmem + (kPagedMaxBatch + 1) * 4);
+    if (e != cudaSuccess) return e;
+    configured_for = device_info().device;
+  }
+  paged_mma_kernel<D, NT><<<a.grid, kPagedThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -502,7 +860,10 @@ PagedView make_paged_view(const dd_paged_cache& c) {
 }
 
 size_t paged_attention_workspace(int B, int Hq, int Hkv, int d, int max_len, bool mass) {
-  return paged_layout(B, Hq, d, max_len, mass, heads_per_block(Hq / Hkv)).total;
+  // the type is not known here: room for either
+  const size_t x = paged_layout(B, Hq, d, max_len, mass, heads_per_block(Hq / Hkv, false)).total;
+  const size_t y = paged_layout(B, Hq, d, max_len, mass, heads_per_block(Hq / Hkv, true)).total;
+  return x > y ? x : y;
 }
 
 int64_t paged_attention_tiles(int B, int Hq, int max_len) {
@@ -521,7 +882,7 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.new_bytes = p.new_stride * e;
   a.lengths = p.lengths;
   a.B = p.B; a.Hq = p.Hq; a.G = p.Hq / c.Hkv;
-  a.heads = heads_per_block(a.G);
+  a.heads = heads_per_block(a.G, c.dtype == DD_BF16);
   a.blocks = (a.G + a.heads - 1) / a.heads;
   a.max_len = p.max_len;
   a.scale2 = (p.scale > 0.f ? p.scale : 1.f / sqrtf((float)c.d)) * kLog2e;
@@ -536,13 +897,14 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   a.scores = p.mass_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   const int64_t tiles = (int64_t)p.B * c.Hkv * a.blocks * ((p.max_len + kTile - 1) / kTile);
-  const int64_t most = min((int64_t)kMaxPagedGrid, (int64_t)device_info().sm_count * 4);
+  const int64_t most = min((int64_t)kMaxPagedGrid,
+                           (int64_t)device_info().sm_count * (c.dtype == DD_BF16 ? 2 : 4));
   a.grid = (int)(tiles < most ? tiles : most);
   const size_t smem = ((size_t)p.B + 1) * 4;
   cudaError_t err;
   if (c.dtype == DD_BF16)
-    err = c.d == 128 ? launch_simt<__nv_bfloat16, 128>(a, smem, stream)
-                     : launch_simt<__nv_bfloat16, 64>(a, smem, stream);
+    err = a.heads > 8 ? (c.d == 128 ? launch_mma<128, 2>(a, smem, stream) : launch_mma<64, 2>(a, smem, stream))
+                      : (c.d == 128 ? launch_mma<128, 1>(a, smem, stream) : launch_mma<64, 1>(a, smem, stream));
   else
     err = c.d == 128 ? launch_simt<float, 128>(a, smem, stream) : launch_simt<float, 64>(a, smem, stream);
   if (err != cudaSuccess) return err;
