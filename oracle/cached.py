@@ -78,15 +78,16 @@ def evict_one(mass, pos, budget, sink, recent):
     return [j if j in kept else next(movers) for j in range(budget)]
 
 
-def beam_candidates(logits, score, done, eos, V):
-    """(score, flat index) of every candidate of one request, best first."""
-    out = []
+def beam_candidates(logits, score, done, eos, V, most):
+    """(minus score, flat index) of the first `most` candidates of one request, best first."""
+    values, places = [], []
     for k in range(len(score)):
         base = float(score[k])
         if not base > -np.inf:
             continue
         if done is not None and done[k]:
-            out.append((-base, k * V + max(eos, 0)))
+            values.append(np.array([base]))
+            places.append(np.array([k * V + max(eos, 0)]))
             continue
         x = np.array(logits[k], dtype=np.float64)
         live = x > -np.inf  # False for NaN
@@ -94,14 +95,19 @@ def beam_candidates(logits, score, done, eos, V):
             continue
         m = x[live].max()
         lse = m + np.log(np.exp(x[live] - m).sum())
-        out += [(-(base + (x[v] - lse)), k * V + int(v)) for v in np.nonzero(live)[0]]
-    return sorted(out)
+        values.append(base + (x[live] - lse))
+        places.append(k * V + np.nonzero(live)[0])
+    if not values:
+        return []
+    values, places = np.concatenate(values), np.concatenate(places)
+    order = np.lexsort((places, -values))[:most]
+    return [(-float(values[i]), int(places[i])) for i in order]
 
 
 def beam_select(logits, score, done=None, eos=-1):
     """logits [K,V], score [K], done [K]: parent, token, score, done of the K best."""
     K, V = logits.shape
-    best = beam_candidates(logits, score, done, eos, V)[:K]
+    best = beam_candidates(logits, score, done, eos, V, K)
     parent, token = np.full(K, -1), np.full(K, -1)
     out, ended = np.full(K, -np.inf), np.zeros(K, dtype=np.uint8)
     for r, (neg, at) in enumerate(best):

@@ -9,17 +9,21 @@
 // Bound: HBM, B K V logits read once.
 #include "dd_common.cuh"
 #include "dd_internal.h"
+#include "dd_tc.cuh"
 
 namespace dd {
 
 namespace {
 
 constexpr int kBeamThreads = 256;
-constexpr int kBeamVecs = 4;  // 16-byte vectors per thread
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamVecs = 8;  // 16-byte vectors per thread: a segment of 128 bytes
+constexpr int kPieceBytes = kBeamThreads * kBeamVecs * 16;
+constexpr int kBeamList = 512;  // candidates ranked by counting
 constexpr uint32_t kNone = 0x007FFFFFu;  // key of -inf
 
 template <typename T>
-constexpr int beam_piece() { return kBeamThreads * kBeamVecs * (16 / (int)sizeof(T)); }
+constexpr int beam_piece() { return kPieceBytes / (int)sizeof(T); }
 
 __device__ __forceinline__ uint32_t logit_key(float x) {
   const uint32_t u = __float_as_uint(x);
@@ -31,137 +35,260 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // NaN is no candidate; -0 ties with 0.
 __device__ __forceinline__ float clean_logit(float x) { return x == x ? x + 0.f : -INFINITY; }
 
-template <typename T, int PV>
-__device__ __forceinline__ void unpack(const uint4& r, float (&x)[PV]) {
-  if constexpr (PV == 4) {
-    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
-    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
-  } else {
-    x[0] = bf16lo(r.x); x[1] = bf16hi(r.x); x[2] = bf16lo(r.y); x[3] = bf16hi(r.y);
-    x[4] = bf16lo(r.z); x[5] = bf16hi(r.z); x[6] = bf16lo(r.w); x[7] = bf16hi(r.w);
-  }
+// The two (bf16) or one (fp32) logits of a 32-bit word.
+template <typename T>
+struct Word;
+template <>
+struct Word<__nv_bfloat16> {
+  static constexpr int n = 2;
+  static __device__ __forceinline__ float get(uint32_t w, int e) { return e ? bf16hi(w) : bf16lo(w); }
+  static constexpr uint32_t kNegInf = 0xFF80FF80u;
+};
+template <>
+struct Word<float> {
+  static constexpr int n = 1;
+  static __device__ __forceinline__ float get(uint32_t w, int) { return __uint_as_float(w); }
+  static constexpr uint32_t kNegInf = 0xFF800000u;
+};
+
+// Largest logit of four words, NaN ignored (NaN only if all are).
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+__device__ __forceinline__ uint32_t max_word(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ float max_of(uint32_t w, __nv_bfloat16) { return fmaxf(bf16lo(w), bf16hi(w)); }
+__device__ __forceinline__ float max_of(uint32_t w, float) { return __uint_as_float(w); }
 
 __device__ __forceinline__ bool scans(const float* score_in, const uint8_t* done_in, int row) {
   const float s = score_in[row];
-  return s > -INFINITY && !(done_in && done_in[row]);
+  const uint8_t d = done_in ? done_in[row] : 0;  // both loads in flight at once
+  return s > -INFINITY && !d;
 }
 
-// One piece of one row. The K-th largest of the 256 threads' maxima is a lower bound of the
-// piece's K-th largest logit, and only the fewer than K threads whose maximum lies above it
-// hold logits above it: those are collected and ranked by counting, and the lowest indices
-// of the logits equal to it (a bitmap) fill up.
+// The largest 16-bit p that at least `want` of the 256 keys reach (0 if fewer are above 0),
+// bit by bit, by one warp.
+__device__ __forceinline__ uint32_t kth_key16(const uint16_t* keys, int want) {
+  const uint4 w = *reinterpret_cast<const uint4*>(keys + (threadIdx.x & 31) * 8);
+  const uint32_t k[8] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16,
+                         w.z & 0xffffu, w.z >> 16, w.w & 0xffffu, w.w >> 16};
+  uint32_t p = 0;
+#pragma unroll
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t c = p | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) n += k[e] >= c;
+    if (__reduce_add_sync(0xffffffffu, n) >= want) p = c;
+  }
+  return p;
+}
+
+// One piece of one row, copied into shared memory by one bulk copy; several CTAs share an
+// SM, so their copies and their arithmetic overlap. A thread reads a segment of the piece
+// (eight vectors), keeps its maximum and sums exponentials relative to that maximum. The
+// K-th largest of the 256 maxima (its top 16 bits) is a lower bound of the piece's K-th
+// largest logit, so only the segments whose maximum reaches it, about K of them, are
+// looked at again, a warp to a segment; what reaches the bound there is ranked by counting.
+// Where more than kBeamList logits reach the bound (long runs of equal logits), the K-th
+// largest is found by a radix select over the piece instead.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads)
+__global__ void __launch_bounds__(kBeamThreads, 6)
 beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pieces,
                  const float* __restrict__ score_in, const uint8_t* __restrict__ done_in,
-                 float2* __restrict__ ml, uint2* __restrict__ cand) {
-  constexpr int PV = 16 / (int)sizeof(T);
+                 float2* __restrict__ ml, uint2* __restrict__ cand, uint32_t spin) {
+  using W = Word<T>;
   constexpr int kPiece = beam_piece<T>();
-  constexpr int kMost = (kBeamMaxK - 1) * kBeamVecs * PV;  // logits above the bound
-  __shared__ uint32_t s_key[kBeamThreads];
-  __shared__ uint32_t s_gt_key[kMost];
-  __shared__ int s_gt_idx[kMost];
-  __shared__ uint32_t s_tie[kPiece / 32];
-  __shared__ float s_red[kBeamThreads / 32];
-  __shared__ int s_scan[kBeamThreads / 32];
+  extern __shared__ __align__(128) uint8_t piece_smem[];  // [kPieceBytes]
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ __align__(16) uint16_t s_key[kBeamThreads];
+  __shared__ uint2 s_list[kBeamList];   // (key, index in the piece)
+  __shared__ uint8_t s_seg[kBeamThreads];
+  __shared__ float2 s_ml[kBeamWarps + kBeamWarps / 2];  // and the radix select's scan
+  __shared__ int s_n, s_segs, s_want;
   __shared__ uint32_t s_bound;
-  __shared__ int s_n;
   const int row = blockIdx.x / pieces, piece = blockIdx.x - row * pieces;
   if (!scans(score_in, done_in, row)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T* x0 = logits + (int64_t)row * ld;
-  const int base = piece * kPiece;
-  uint4 raw[kBeamVecs];
+  const int base = piece * kPiece, n_here = min(kPiece, V - base);
+  uint32_t* words = reinterpret_cast<uint32_t*>(piece_smem);
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    tc::fence_barrier_init();
+    const uint32_t bytes = ((uint32_t)n_here * sizeof(T) + 15u) & ~15u;
+    tc::mbar_expect_tx(&bar, bytes);
+    tc::bulk_load(piece_smem, logits + (int64_t)row * ld + base, bytes, &bar);
+    s_n = 0;
+    s_segs = 0;
+  }
+  __syncthreads();
+  const bool here = mbar_wait_bounded(&bar, 0, spin);
+  if (__syncthreads_or(!here)) return;  // recorded; uniform over the CTA
+  if (n_here < kPiece) {
+    T* x = reinterpret_cast<T*>(piece_smem);
+    for (int i = n_here + threadIdx.x; i < kPiece; i += kBeamThreads) x[i] = static_cast<T>(-INFINITY);
+    __syncthreads();
+  }
+  const uint4* seg = reinterpret_cast<const uint4*>(piece_smem) + threadIdx.x;  // every 256th vector
+  uint32_t mw[4] = {W::kNegInf, W::kNegInf, W::kNegInf, W::kNegInf};
 #pragma unroll
   for (int i = 0; i < kBeamVecs; ++i) {
-    const int v = base + (i * kBeamThreads + threadIdx.x) * PV;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (v < V) raw[i] = *reinterpret_cast<const uint4*>(x0 + v);
+    const uint4 v = seg[i * kBeamThreads];
+    mw[0] = max_word(mw[0], v.x, T{});
+    mw[1] = max_word(mw[1], v.y, T{});
+    mw[2] = max_word(mw[2], v.z, T{});
+    mw[3] = max_word(mw[3], v.w, T{});
   }
-  const auto each = [&](auto f) {
-#pragma unroll
+  const float mx = max_of(max_word(max_word(mw[0], mw[1], T{}), max_word(mw[2], mw[3], T{}), T{}), T{}) + 0.f;
+  const uint32_t mine = logit_key(mx) >> 16;
+  s_key[threadIdx.x] = (uint16_t)mine;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t p = kth_key16(s_key, K);
+    if (lane == 0) s_bound = p;
+  }
+  // sum of exponentials relative to the segment's maximum
+  const float ref2 = mx * kLog2e;  // rounded once: the sum is relative to exactly 2^ref2
+  const float ref = mx > -INFINITY ? ref2 : 0.f;
+  float sum = 0.f;
+  {
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
     for (int i = 0; i < kBeamVecs; ++i) {
-      float x[PV];
-      unpack<T, PV>(raw[i], x);
-      const int at = (i * kBeamThreads + threadIdx.x) * PV;
+      const uint4 v = seg[i * kBeamThreads];
+      const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < PV; ++e) f(base + at + e < V ? clean_logit(x[e]) : -INFINITY, at + e);
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int h = 0; h < W::n; ++h) part[e] += fast_exp2(fmaf(W::get(r[e], h), kLog2e, -ref));
     }
-  };
-  float mx = -INFINITY;
-  each([&](float x, int) { mx = fmaxf(mx, x); });
-  s_key[threadIdx.x] = logit_key(mx);
-  for (int i = threadIdx.x; i < kPiece / 32; i += kBeamThreads) s_tie[i] = 0u;
-  float m = mx;
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+    if (sum != sum) {  // NaN logits add nothing
+      sum = 0.f;
+      for (int i = 0; i < kBeamVecs; ++i) {
+        const uint4 v = seg[i * kBeamThreads];
+        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int h = 0; h < W::n; ++h)
+            sum += fast_exp2(fmaf(clean_logit(W::get(r[e], h)), kLog2e, -ref));
+      }
+    }
+  }
+  // (maximum, sum) of the piece, log2 units
+  float m = ref2;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) s_red[warp] = m;
-  if (threadIdx.x == 0) { s_bound = kNone; s_n = 0; }
-  __syncthreads();
-  m = s_red[0];
-#pragma unroll
-  for (int w = 1; w < kBeamThreads / 32; ++w) m = fmaxf(m, s_red[w]);
-  const float mb = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  each([&](float x, int) { sum += exp2f((x - mb) * kLog2e); });
+  sum *= mx > -INFINITY ? fast_exp2(ref2 - m) : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  // the K-th largest thread maximum
-  const uint32_t mine = s_key[threadIdx.x];
-  int above = 0;
-  for (int t = 0; t < kBeamThreads; ++t) {
-    const uint32_t k = s_key[t];
-    above += k > mine || (k == mine && t < (int)threadIdx.x);
-  }
-  if (above == K - 1) s_bound = mine;
+  if (lane == 0) s_ml[warp] = make_float2(m, sum);
   __syncthreads();
-  if (lane == 0) s_red[warp] = sum;
   const uint32_t bound = s_bound;
-  if (mine >= bound && mine > kNone)
-    each([&](float x, int at) {
-      const uint32_t k = logit_key(x);
-      if (k > bound) {
-        const int i = atomicAdd(&s_n, 1);
-        if (DD_IN_BOUNDS(i < kMost)) { s_gt_key[i] = k; s_gt_idx[i] = at; }
-      } else if (k == bound && bound > kNone) {
-        atomicOr(&s_tie[at >> 5], 1u << (at & 31));
-      }
-    });
+  if (mine >= bound && mx > -INFINITY) s_seg[atomicAdd(&s_segs, 1)] = (uint8_t)threadIdx.x;
   __syncthreads();
-  const int n = min(s_n, kMost);
+  const int segs = s_segs;
+  for (int i = warp; i < segs; i += kBeamWarps) {
+    const int t = s_seg[i];
+    // word `lane` of the segment: vector lane / 4, word lane % 4
+    const int at = (((lane >> 2) * kBeamThreads + t) << 2) + (lane & 3);
+    const uint32_t w = words[at];
+#pragma unroll
+    for (int h = 0; h < W::n; ++h) {
+      const uint32_t k = logit_key(clean_logit(W::get(w, h)));
+      const bool in = (k >> 16) >= bound && k > kNone;
+      const uint32_t mask = __ballot_sync(0xffffffffu, in);
+      if (!mask) continue;
+      int first = 0;
+      if (lane == 0) first = atomicAdd(&s_n, __popc(mask));
+      first = __shfl_sync(0xffffffffu, first, 0) + __popc(mask & ((1u << lane) - 1u));
+      if (in && first < kBeamList) s_list[first] = make_uint2(k, (uint32_t)(at * W::n + h));
+    }
+  }
+  __syncthreads();
+  int n = s_n;
+  if (n > kBeamList) {
+    // ---- radix select over the piece
+    int* hist = reinterpret_cast<int*>(s_list);  // the list is empty again
+    int* scan = reinterpret_cast<int*>(s_ml + kBeamWarps);
+    const T* x = reinterpret_cast<const T*>(piece_smem);
+    uint32_t prefix = 0u;
+    int want = K;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      const uint32_t hmask = shift == 24 ? 0u : (0xFFFFFFFFu << (shift + 8));
+      hist[threadIdx.x] = 0;
+      __syncthreads();
+      for (int i = threadIdx.x; i < kPiece; i += kBeamThreads) {
+        const uint32_t k = logit_key(clean_logit((float)x[i]));
+        if (k > kNone && (k & hmask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int run = 0, dgt = 255;
+        for (; dgt > 0 && run + hist[dgt] < want; --dgt) run += hist[dgt];
+        s_bound = prefix | ((uint32_t)dgt << shift);
+        s_want = want - run;
+      }
+      __syncthreads();
+      prefix = s_bound;
+      want = s_want;
+    }
+    // more than kBeamList >= K logits are candidates, so `prefix` is the K-th largest key and
+    // `want` >= 1 of the logits equal to it are taken, from the lowest index
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();  // also: the histogram is read
+    constexpr int kRun = kPiece / kBeamThreads;
+    int ties = 0;
+    for (int i = threadIdx.x * kRun; i < (threadIdx.x + 1) * kRun; ++i) {
+      const uint32_t k = logit_key(clean_logit((float)x[i]));
+      if (k > prefix) {
+        const int at = atomicAdd(&s_n, 1);
+        if (DD_IN_BOUNDS(at < kBeamList)) s_list[at] = make_uint2(k, (uint32_t)i);
+      }
+      ties += k == prefix;
+    }
+    int incl = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int before = incl - ties;
+    for (int w = 0; w < warp; ++w) before += scan[w];
+    const int above = s_n;
+    for (int i = threadIdx.x * kRun; i < (threadIdx.x + 1) * kRun && before < want; ++i)
+      if (logit_key(clean_logit((float)x[i])) == prefix) {
+        if (DD_IN_BOUNDS(above + before < kBeamList)) s_list[above + before] = make_uint2(prefix, (uint32_t)i);
+        ++before;
+      }
+    __syncthreads();
+    n = min(above + want, kBeamList);
+  }
   uint2* out = cand + (int64_t)blockIdx.x * K;
   for (int i = threadIdx.x; i < n; i += kBeamThreads) {
-    const uint32_t k = s_gt_key[i];
-    const int at = s_gt_idx[i];
+    const uint2 c = s_list[i];
     int r = 0;
-    for (int t = 0; t < n; ++t) r += s_gt_key[t] > k || (s_gt_key[t] == k && s_gt_idx[t] < at);
-    if (r < K) out[r] = make_uint2(k, (uint32_t)(base + at));
+    for (int t = 0; t < n; ++t) {
+      const uint2 o = s_list[t];
+      r += o.x > c.x || (o.x == c.x && o.y < c.y);
+    }
+    if (r < K) out[r] = make_uint2(c.x, (uint32_t)base + c.y);
   }
-  // ties fill up from the lowest index
-  uint32_t bits = threadIdx.x < kPiece / 32 ? s_tie[threadIdx.x] : 0u;
-  const int cnt = __popc(bits);
-  int incl = cnt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int r = n + incl - cnt, all = n;
-#pragma unroll
-  for (int w = 0; w < kBeamThreads / 32; ++w) {
-    if (w < warp) r += s_scan[w];
-    all += s_scan[w];
-  }
-  for (; bits && r < K; ++r, bits &= bits - 1u)
-    out[r] = make_uint2(bound, (uint32_t)(base + threadIdx.x * 32 + __ffs(bits) - 1));
-  for (int i = all + threadIdx.x; i < K; i += kBeamThreads) out[i] = make_uint2(kNone, 0u);
+  for (int i = n + threadIdx.x; i < K; i += kBeamThreads) out[i] = make_uint2(kNone, 0u);
   if (threadIdx.x == 0) {
+    m = s_ml[0].x;
+#pragma unroll
+    for (int w = 1; w < kBeamWarps; ++w) m = fmaxf(m, s_ml[w].x);
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kBeamThreads / 32; ++w) s += s_red[w];
+    for (int w = 0; w < kBeamWarps; ++w)
+      if (s_ml[w].x > -INFINITY) s = fmaf(s_ml[w].y, fast_exp2(s_ml[w].x - m), s);
     ml[blockIdx.x] = make_float2(m, s);
   }
 }
@@ -175,112 +302,215 @@ __device__ __forceinline__ bool better(double s, int64_t at, double s2, int64_t 
   return s > s2 || (s == s2 && at < at2);
 }
 
-// One CTA per request: K rounds, each taking the best head of the sorted lists (one per
-// beam and piece) and stepping that list on.
+// What the merge holds on chip from its first loads: entries per thread, and the sums of
+// rows of up to so many pieces (more are read again where they are needed).
+constexpr int kHeldEntries = 12;
+constexpr int kHeldPieces = 24;
+
+struct BeamOut {
+  int32_t* parent;
+  int32_t* token;
+  float* score;
+  uint8_t* done;
+  int eos;
+};
+// Rank r of request b: candidate `at` = k V + v of beam k (k < 0: none).
+__device__ __forceinline__ void write_beam(const BeamOut& o, int64_t r, int k, bool was_done, double score,
+                                           int64_t at, int V) {
+  const int v = k < 0 ? -1 : was_done ? o.eos : (int)(at - (int64_t)k * V);
+  o.parent[r] = k < 0 ? -1 : k;
+  o.token[r] = v;
+  o.score[r] = k < 0 ? -INFINITY : (float)score;
+  if (o.done) o.done[r] = k >= 0 && (was_done || v == o.eos) ? 1 : 0;
+}
+
+// One CTA per request. Candidates are the lists' entries (K per beam and piece) and one of
+// each beam that is done. The K-th largest of the threads' best scores bounds the K-th best
+// from below; the few candidates that reach it are ranked by counting. (The bound compares
+// distances below the best score by their top 16 bits: 1 part in 128, whatever the scores'
+// size.) Should more than kBeamList reach it, K rounds over the lists' heads pick one each.
 __global__ void __launch_bounds__(kBeamThreads)
 beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
-                  const uint8_t* __restrict__ done_in, int eos, const float2* __restrict__ ml,
-                  const uint2* __restrict__ cand, int32_t* __restrict__ parent,
-                  int32_t* __restrict__ token, float* __restrict__ score_out,
-                  uint8_t* __restrict__ done_out) {
+                  const uint8_t* __restrict__ done_in, const float2* __restrict__ ml,
+                  const uint2* __restrict__ cand, BeamOut res) {
   pdl_wait();
   extern __shared__ uint8_t head[];  // [K * pieces]
   __shared__ double s_base[kBeamMaxK];
   __shared__ uint8_t s_kind[kBeamMaxK];  // 0 no candidate, 1 live, 2 done
-  __shared__ Best s_best[kBeamThreads / 32];
+  __shared__ Best s_best[kBeamWarps];
+  __shared__ float2 s_ml[kBeamMaxK * kHeldPieces];
+  __shared__ double s_score[kBeamList];
+  __shared__ int64_t s_at[kBeamList];
+  __shared__ __align__(16) uint16_t s_key[kBeamThreads];
+  __shared__ uint32_t s_bound;
+  __shared__ int s_n;
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int k = warp; k < K; k += kBeamThreads / 32) {
-    const int row = b * K + k;
-    const float s = score_in[row];
-    if (!scans(score_in, done_in, row)) {
-      if (lane == 0) {
-        s_kind[k] = s > -INFINITY ? 2 : 0;
-        s_base[k] = (double)s;
-      }
-      continue;
-    }
+  const int lists = K * pieces, entries = lists * K;
+  const uint2* mine = cand + (int64_t)b * entries;
+  // everything is loaded at once: the lists' entries do not wait for the sums
+  uint2 held[kHeldEntries];
+#pragma unroll
+  for (int e = 0; e < kHeldEntries; ++e) {
+    const int i = e * kBeamThreads + threadIdx.x;
+    held[e] = i < entries ? mine[i] : make_uint2(kNone, 0u);
+  }
+  const bool small = pieces <= kHeldPieces;
+  if (small)
+    for (int i = threadIdx.x; i < lists; i += kBeamThreads) s_ml[i] = ml[(int64_t)b * lists + i];
+  if (threadIdx.x < K) {
+    const float s = score_in[b * K + threadIdx.x];
+    const bool done = done_in && done_in[b * K + threadIdx.x];
+    s_kind[threadIdx.x] = !(s > -INFINITY) ? 0 : done ? 2 : 1;
+    s_base[threadIdx.x] = (double)s;
+  }
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  for (int k = warp; k < K; k += kBeamWarps) {
+    if (s_kind[k] != 1) continue;
+    const float2* p = small ? s_ml + k * pieces : ml + ((int64_t)b * K + k) * pieces;
     float m = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, ml[(int64_t)row * pieces + i].x);
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, p[i].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     double z = 0.0;
     if (m > -INFINITY)
-      for (int i = lane; i < pieces; i += 32) {
-        const float2 p = ml[(int64_t)row * pieces + i];
-        z += (double)p.y * exp((double)p.x - (double)m);
-      }
+      for (int i = lane; i < pieces; i += 32) z += (double)p[i].y * (double)exp2f(p[i].x - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    __syncwarp();
     if (lane == 0) {
-      s_kind[k] = m > -INFINITY ? 1 : 0;
-      s_base[k] = (double)s - ((double)m + log(z));
+      if (m > -INFINITY) s_base[k] -= (double)m / (double)kLog2e + log(z);
+      else s_kind[k] = 0;
     }
   }
-  const int lists = K * pieces;
+  __syncthreads();
+  // candidate i: entry i of the lists, or the one of done beam i - entries
+  const auto score_of = [&](int i, const uint2& c, double& s, int64_t& at) {
+    const int k = i / (pieces * K);
+    if (s_kind[k] != 1 || c.x <= kNone) return false;
+    s = s_base[k] + (double)key_logit(c.x);
+    at = (int64_t)k * V + c.y;
+    return true;
+  };
+  const auto get = [&](int i, double& s, int64_t& at) {
+    if (i < entries) return score_of(i, mine[i], s, at);
+    const int k = i - entries;
+    if (s_kind[k] != 2) return false;
+    s = s_base[k];
+    at = (int64_t)k * V + (res.eos > 0 ? res.eos : 0);
+    return true;
+  };
+  const auto each = [&](auto f) {  // of this thread's candidates
+    double s;
+    int64_t at;
+#pragma unroll
+    for (int e = 0; e < kHeldEntries; ++e) {
+      const int i = e * kBeamThreads + threadIdx.x;
+      if (held[e].x > kNone && score_of(i, held[e], s, at)) f(s, at);
+    }
+    for (int i = kHeldEntries * kBeamThreads + threadIdx.x; i < entries; i += kBeamThreads)
+      if (get(i, s, at)) f(s, at);
+    if (threadIdx.x < K && get(entries + threadIdx.x, s, at)) f(s, at);
+  };
+  double top = -INFINITY;
+  each([&](double s, int64_t) { top = fmax(top, s); });
+  double best = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = fmax(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) s_best[warp].score = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kBeamWarps; ++w) best = fmax(best, s_best[w].score);
+  const auto near = [&](double s) {  // 16 bits, larger nearer to the best; 0: none
+    return s > -INFINITY ? 0xFFFFu - (__float_as_uint((float)(best - s)) >> 16) : 0u;
+  };
+  s_key[threadIdx.x] = (uint16_t)near(top);
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t p = kth_key16(s_key, K);
+    if (lane == 0) s_bound = p;
+  }
+  __syncthreads();
+  const uint32_t bound = s_bound;
+  if (s_key[threadIdx.x] >= bound)
+    each([&](double s, int64_t at) {
+      if (near(s) < bound) return;
+      const int n = atomicAdd(&s_n, 1);
+      if (n < kBeamList) {
+        s_score[n] = s;
+        s_at[n] = at;
+      }
+    });
+  __syncthreads();
+  const int n = s_n;
+  if (n <= kBeamList) {
+    for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+      const double s = s_score[i];
+      const int64_t at = s_at[i];
+      int r = 0;
+      for (int t = 0; t < n; ++t) r += better(s_score[t], s_at[t], s, at);
+      const int k = (int)(at / V);
+      if (r < K) write_beam(res, (int64_t)b * K + r, k, s_kind[k] == 2, s, at, V);
+    }
+    for (int r = n + threadIdx.x; r < K; r += kBeamThreads)
+      write_beam(res, (int64_t)b * K + r, -1, false, 0.0, 0, V);
+    return;
+  }
+  // ---- K rounds: the best head of the sorted lists, whose list steps on
   for (int i = threadIdx.x; i < lists; i += kBeamThreads) head[i] = 0;
   __syncthreads();
-  const auto find = [&](Best& best) {
-    best = Best{-INFINITY, INT64_MAX, -1};
+  const auto find = [&](Best& o) {
+    o = Best{-INFINITY, INT64_MAX, -1};
     for (int i = threadIdx.x; i < lists; i += kBeamThreads) {
       const int k = i / pieces, h = head[i];
       double s;
       int64_t at;
-      if (s_kind[k] == 1) {
-        if (h >= K) continue;
-        const uint2 c = cand[((int64_t)b * lists + i) * K + h];
-        if (c.x <= kNone) continue;
-        s = s_base[k] + (double)key_logit(c.x);
-        at = (int64_t)k * V + c.y;
-      } else {
-        if (s_kind[k] == 0 || i != k * pieces || h > 0) continue;
-        s = s_base[k];
-        at = (int64_t)k * V + (eos > 0 ? eos : 0);
-      }
-      if (better(s, at, best.score, best.at)) best = Best{s, at, i};
+      if (s_kind[k] == 1 ? h < K && get(i * K + h, s, at)
+                         : h == 0 && i == k * pieces && get(entries + k, s, at))
+        if (better(s, at, o.score, o.at)) o = Best{s, at, i};
     }
   };
   Best own;
   find(own);
   for (int r = 0; r < K; ++r) {
-    Best best = own;
+    Best x = own;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double s = __shfl_xor_sync(0xffffffffu, best.score, o);
-      const int64_t at = __shfl_xor_sync(0xffffffffu, best.at, o);
-      const int list = __shfl_xor_sync(0xffffffffu, best.list, o);
-      if (better(s, at, best.score, best.at)) best = Best{s, at, list};
+      const double s = __shfl_xor_sync(0xffffffffu, x.score, o);
+      const int64_t at = __shfl_xor_sync(0xffffffffu, x.at, o);
+      const int list = __shfl_xor_sync(0xffffffffu, x.list, o);
+      if (better(s, at, x.score, x.at)) x = Best{s, at, list};
     }
-    if (lane == 0) s_best[warp] = best;
+    if (lane == 0) s_best[warp] = x;
     __syncthreads();
-    best = s_best[0];
-    for (int w = 1; w < kBeamThreads / 32; ++w)
-      if (better(s_best[w].score, s_best[w].at, best.score, best.at)) best = s_best[w];
+    x = s_best[0];
+    for (int w = 1; w < kBeamWarps; ++w)
+      if (better(s_best[w].score, s_best[w].at, x.score, x.at)) x = s_best[w];
     __syncthreads();
-    const bool found = best.list >= 0;
     if (threadIdx.x == 0) {
-      const int64_t o = (int64_t)b * K + r;
-      const int k = found ? best.list / pieces : -1;
-      const bool was_done = found && s_kind[k] == 2;
-      const int v = !found ? -1 : was_done ? eos : (int)(best.at - (int64_t)k * V);
-      parent[o] = k;
-      token[o] = v;
-      score_out[o] = found ? (float)best.score : -INFINITY;
-      if (done_out) done_out[o] = was_done || (found && v == eos) ? 1 : 0;
+      const int k = x.list >= 0 ? x.list / pieces : -1;
+      write_beam(res, (int64_t)b * K + r, k, k >= 0 && s_kind[k] == 2, x.score, x.at, V);
     }
-    if (found && best.list % kBeamThreads == (int)threadIdx.x) {
-      head[best.list] += 1;
+    if (x.list >= 0 && x.list % kBeamThreads == (int)threadIdx.x) {
+      head[x.list] += 1;
       find(own);
     }
   }
 }
 
-}  // namespace
-
-namespace {
 int beam_pieces(int V, dd_dtype dtype) {
   const int piece = dtype == DD_BF16 ? beam_piece<__nv_bfloat16>() : beam_piece<float>();
   return (V + piece - 1) / piece;
 }
+
+template <typename T>
+cudaError_t launch_scan(const BeamCall& p, unsigned grid, int pieces, float2* ml, uint2* cand,
+                        cudaStream_t stream) {
+  beam_scan_kernel<T><<<grid, kBeamThreads, kPieceBytes, stream>>>(
+      static_cast<const T*>(p.logits), p.K, p.V, p.ld, pieces, p.score_in, p.done_in, ml, cand, spin_limit());
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t beam_select_workspace(int B, int K, int V, dd_dtype dtype) {
@@ -293,13 +523,8 @@ cudaError_t launch_beam_select(const BeamCall& p, cudaStream_t stream) {
   const size_t lists = (size_t)p.B * p.K * pieces;
   float2* ml = static_cast<float2*>(p.workspace);
   uint2* cand = reinterpret_cast<uint2*>(static_cast<char*>(p.workspace) + ((lists * 8 + 255) & ~(size_t)255));
-  if (p.dtype == DD_BF16)
-    beam_scan_kernel<__nv_bfloat16><<<(unsigned)lists, kBeamThreads, 0, stream>>>(
-        static_cast<const __nv_bfloat16*>(p.logits), p.K, p.V, p.ld, pieces, p.score_in, p.done_in, ml, cand);
-  else
-    beam_scan_kernel<float><<<(unsigned)lists, kBeamThreads, 0, stream>>>(
-        static_cast<const float*>(p.logits), p.K, p.V, p.ld, pieces, p.score_in, p.done_in, ml, cand);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = p.dtype == DD_BF16 ? launch_scan<__nv_bfloat16>(p, (unsigned)lists, pieces, ml, cand, stream)
+                                     : launch_scan<float>(p, (unsigned)lists, pieces, ml, cand, stream);
   if (e != cudaSuccess) return e;
   static thread_local int configured_for = -1;
   if (configured_for != device_info().device) {
@@ -308,9 +533,9 @@ cudaError_t launch_beam_select(const BeamCall& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_for = device_info().device;
   }
+  const BeamOut res{p.parent, p.token, p.score_out, p.done_out, p.eos};
   return launch_dependent(beam_merge_kernel, dim3(p.B), dim3(kBeamThreads), (size_t)p.K * pieces, stream, p.K,
-                          p.V, pieces, p.score_in, p.done_in, p.eos, (const float2*)ml, (const uint2*)cand,
-                          p.parent, p.token, p.score_out, p.done_out);
+                          p.V, pieces, p.score_in, p.done_in, (const float2*)ml, (const uint2*)cand, res);
 }
 
 }  // namespace dd

@@ -228,6 +228,7 @@ __device__ __forceinline__ void copy_units(char* dst, const char* src, int64_t b
 __global__ void __launch_bounds__(kCopyThreads)
 beam_reorder_kernel(const int32_t* __restrict__ parent, int K,
                     const __grid_constant__ RowStates st) {
+  pdl_wait();
   const dd_row_state& s = st.s[blockIdx.y];
   const int n = blockIdx.x, p = parent_row(parent, n, K);
   const char* src = static_cast<const char*>(s.src) + (int64_t)p * s.src_stride;
@@ -246,6 +247,7 @@ paged_fork_kernel(PagedView c, const int32_t* __restrict__ parent, int K,
                   const int32_t* __restrict__ lengths, const int32_t* __restrict__ fresh,
                   int32_t* __restrict__ table_out, int64_t out_stride,
                   int32_t* __restrict__ lengths_out, int chunk16_log2) {
+  pdl_wait();
   const int n = blockIdx.x, p = parent_row(parent, n, K);
   const int len = checked_length(lengths, p, c.cap);
   const int full = div_fast(c.page, len), rest = len - full * c.page.n;
@@ -327,9 +329,8 @@ cudaError_t launch_beam_reorder(const int32_t* parent, int B, int K, const dd_ro
   }
   int64_t parts = (longest + kCopyThreads * 16 - 1) / (kCopyThreads * 16);
   if (parts > 64) parts = 64;
-  beam_reorder_kernel<<<dim3((unsigned)rows, n_states, (unsigned)parts), kCopyThreads, 0, stream>>>(
-      parent, K, st);
-  return cudaGetLastError();
+  return launch_dependent(beam_reorder_kernel, dim3((unsigned)rows, n_states, (unsigned)parts),
+                          dim3(kCopyThreads), 0, stream, parent, K, st);
 }
 
 cudaError_t launch_paged_fork(const dd_paged_cache& cache, const int32_t* parent, int B, int K,
@@ -339,9 +340,9 @@ cudaError_t launch_paged_fork(const dd_paged_cache& cache, const int32_t* parent
   const int64_t units = (int64_t)(cache.page_size - 1) * (cache.Hkv << lg);
   int64_t parts = (units + kCopyThreads * 4 - 1) / (kCopyThreads * 4);
   parts = parts < 1 ? 1 : parts > 64 ? 64 : parts;
-  paged_fork_kernel<<<dim3(B * K, cache.layers, (unsigned)parts), kCopyThreads, 0, stream>>>(
-      make_paged_view(cache), parent, K, lengths, fresh, table_out, out_stride, lengths_out, lg);
-  return cudaGetLastError();
+  return launch_dependent(paged_fork_kernel, dim3(B * K, cache.layers, (unsigned)parts),
+                          dim3(kCopyThreads), 0, stream, make_paged_view(cache), parent, K, lengths,
+                          fresh, table_out, out_stride, lengths_out, lg);
 }
 
 }  // namespace dd

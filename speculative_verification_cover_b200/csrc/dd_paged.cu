@@ -47,7 +47,7 @@ struct PagedArgs {
   float2* part_ml;             // [2 grid][heads] (m, l) of the partial results, log2 units
   float* part_o;               // [2 grid][heads][d]
   float* lse2;                 // [B, Hq] in log2 units, of unsplit sequence-heads
-  float* scores;               // [B, Hkv, max_len, G], log2 units (masses only)
+  float* scores;               // [B, Hq, max_len], log2 units (masses only)
   int grid;
 };
 
@@ -253,7 +253,7 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
       const int c = lane >> SH, iu = c / GB, ig = c % GB;
       const float sc = (held >> iu) & 1u ? s[0] : -INFINITY;
       if (a.scores && (lane & ((1 << SH) - 1)) == 0 && ig < nh && j + iu < j1)
-        a.scores[(((int64_t)b * a.c.Hkv + kvh) * a.max_len + j + iu) * a.G + blk * a.heads + ig] = sc;
+        a.scores[((int64_t)b * a.Hq + h0 + ig) * a.max_len + j + iu] = sc;
       float mx = sc;
 #pragma unroll
       for (int bit = 16; bit >= 32 / U; bit >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, bit));
@@ -392,9 +392,10 @@ struct MmaCfg {
   static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;  // two CTAs per SM
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalf = kWarpSlots * kRowBytes;  // K, or V, of one stage
-  static constexpr int kRing = kPagedWarps * kStages * 2 * kHalf;
-  static constexpr int kJoin = kPagedWarps * NT * 8 * (D + 4) * 4;
-  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kSmem = kPagedWarps * kStages * 2 * kHalf;
+  // a warp's results at the end of a sequence-head, [heads][d] fp32, go where its last
+  // stage was
+  static_assert(NT * 8 * D * 4 <= 2 * kHalf);
 };
 
 template <int D, int NT>
@@ -408,7 +409,6 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int warp_tmp[kPagedWarps];
   __shared__ float s_m[kPagedWarps][H], s_l[kPagedWarps][H];
-  float* s_o = reinterpret_cast<float*>(smem + C::kRing);  // [warp][head][D + 4]
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = plan_tiles(a, prefix, warp_tmp);
@@ -541,15 +541,11 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         if (a.scores) {
           const int j = (tile0 + i) * kTile + warp * kWarpSlots + (lane >> 2);
           const int g = t * 8 + 2 * (lane & 3);
-          float* sp = a.scores + (((int64_t)b * a.c.Hkv + kvh) * a.max_len + j) * a.G + blk * a.heads + g;
-          if (j < len) {
-            if (g < nh) sp[0] = s[t][0];
-            if (g + 1 < nh) sp[1] = s[t][1];
-          }
-          if (j + 8 < len) {
-            if (g < nh) sp[8 * (int64_t)a.G] = s[t][2];
-            if (g + 1 < nh) sp[8 * (int64_t)a.G + 1] = s[t][3];
-          }
+          float* sp = a.scores + ((int64_t)b * a.Hq + h0 + g) * a.max_len + j;
+          if (g < nh && j < len) sp[0] = s[t][0];
+          if (g < nh && j + 8 < len) sp[8] = s[t][2];
+          if (g + 1 < nh && j < len) sp[a.max_len] = s[t][1];
+          if (g + 1 < nh && j + 8 < len) sp[a.max_len + 8] = s[t][3];
         }
         float mx[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
         float p[4];
@@ -605,7 +601,14 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         l[t][e] = x;
       }
-    __syncthreads();  // the previous piece's reads are over
+    // the stage read last is free until the next copy into it, which comes after the join;
+    // element e of a head's row lies at e ^ (8 * (head / 2 % 4)), which spreads the heads a
+    // warp writes at once over the banks
+    const int last = stage == 0 ? C::kStages - 1 : stage - 1;
+    const auto joined = [&](int w) {
+      return reinterpret_cast<float*>(smem + (w * C::kStages + last) * 2 * C::kHalf);
+    };
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -615,11 +618,12 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
           s_m[warp][g] = m[t][e];
           s_l[warp][g] = l[t][e];
         }
-        float* op = s_o + (warp * H + g) * (D + 4) + (lane >> 2);
+        float* op = joined(warp) + g * D;
+        const int x = (lane & 3) << 3;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          op[k * 16] = o[k][t][e];
-          op[k * 16 + 8] = o[k][t][e + 2];
+          op[(k * 16 + (lane >> 2)) ^ x] = o[k][t][e];
+          op[(k * 16 + 8 + (lane >> 2)) ^ x] = o[k][t][e + 2];
         }
       }
     __syncthreads();
@@ -637,7 +641,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
       for (int w = 0; w < kPagedWarps; ++w) {
         const float f = exp2f(s_m[w][g] - base);
         ll = fmaf(s_l[w][g], f, ll);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * H + g) * (D + 4) + e);
+        const float4 x = *reinterpret_cast<const float4*>(joined(w) + g * D + (e ^ (((g >> 1) & 3) << 3)));
         oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
         oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
       }
@@ -658,6 +662,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     }
     u += n_tiles;
     if (u < u_end) {
+      __syncthreads();  // every warp has read the results: the stage is free
       cc.tile = tile0 + n_tiles - 1;
       cc.next(a, prefix, u);
     }
@@ -685,92 +690,138 @@ __device__ __forceinline__ int64_t part_slot(const Span& s, int c) {
 }
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kMassChunk = 256;  // slots per step of a mass CTA
 
+// (m, l) of the union of two parts.
+__device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2) {
+  const float mn = fmaxf(m, m2);
+  const float base = mn == -INFINITY ? 0.f : mn;
+  l = l * exp2f(m - base) + l2 * exp2f(m2 - base);
+  m = mn;
+}
+
+// CTAs [0, B Hq): the output of one (sequence, query head) that was split, its parts over
+// four warps. The rest, mass_ctas to a sequence: the masses, from the scores the main
+// kernel left and the joined log-sums, which each CTA forms for its sequence (4 lanes to a
+// head) rather than waiting for another kernel's.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_join_kernel(const __grid_constant__ PagedArgs a, int out_ctas, int mass_ctas) {
+paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
   pdl_wait();
   constexpr int N = D / 32;
-  extern __shared__ float z2[];  // [Hq] of this sequence, log2 units (mass CTAs)
+  extern __shared__ float z2[];  // [Hq rounded up to 8] of this sequence, log2 units (mass CTAs)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if ((int)blockIdx.x < out_ctas) {  // one warp per (sequence, query head)
-    const int64_t i = (int64_t)blockIdx.x * (kJoinThreads / 32) + warp;
-    if (i >= (int64_t)a.B * a.Hq) return;
-    const int b = (int)(i / a.Hq), h = (int)(i - (int64_t)b * a.Hq);
+  const int64_t heads = (int64_t)a.B * a.Hq;
+  if (blockIdx.x < heads) {
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float s_o[kJoinWarps][D];
+    const int i = blockIdx.x, b = i / a.Hq, h = i - b * a.Hq;
     const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
     const Span s = split_of(a, b, kvh * a.blocks + blk);
     if (s.tiles == 0 || s.c0 == s.c1) return;  // already whole
-    float m = -INFINITY;
-    for (int c = s.c0 + lane; c <= s.c1; c += 32)
-      m = fmaxf(m, a.part_ml[part_slot(s, c) * a.heads + gi].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[N];
+    float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int c = s.c0; c <= s.c1; ++c) {
-      const int64_t at = part_slot(s, c) * a.heads + gi;
-      const float2 ml = a.part_ml[at];
-      const float f = exp2f(ml.x - base);
-      const auto x = load_vec<N>(a.part_o + at * D + lane * N);
-      l = fmaf(ml.y, f, l);
+    for (int c = s.c0 + warp; c <= s.c1; c += 4 * kJoinWarps) {
+      float2 ml[4];
+      LaneRow<float, N> x[4];
 #pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = fmaf(x.v[e], f, acc[e]);
+      for (int k = 0; k < 4; ++k) {
+        const int cc = c + k * kJoinWarps;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (cc > s.c1) continue;
+        const int64_t at = part_slot(s, cc) * a.heads + gi;
+        ml[k] = a.part_ml[at];
+        x[k] = load_vec<N>(a.part_o + at * D + lane * N);
+      }
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f0 = exp2f(m - base);
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (c + k * kJoinWarps > s.c1) continue;
+        const float f = exp2f(ml[k].x - base);
+        l = fmaf(ml[k].y, f, l);
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(x[k].v[e], f, acc[e]);
+      }
+      m = mn;
     }
-    T* out = reinterpret_cast<T*>(a.out) + i * D + lane * N;
+    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
 #pragma unroll
-    for (int e = 0; e < N; ++e) store_out(out + e, l > 0.f ? acc[e] / l : 0.f);
-    if (lane == 0 && a.lse) a.lse[i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int e = 0; e < N; ++e) s_o[warp][lane * N + e] = acc[e];
+    __syncthreads();
+    m = s_m[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w]);
+    const float base = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+    float o = 0.f;
+    const int e = threadIdx.x < D ? threadIdx.x : 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = exp2f(s_m[w] - base);
+      l = fmaf(s_l[w], f, l);
+      o = fmaf(s_o[w][e], f, o);
+    }
+    if (threadIdx.x < D) store_out(reinterpret_cast<T*>(a.out) + (int64_t)i * D + e, l > 0.f ? o / l : 0.f);
+    if (threadIdx.x == 0 && a.lse) a.lse[i] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     return;
   }
   // ---- masses of one sequence's slots
-  const int k = blockIdx.x - out_ctas, b = k / mass_ctas, part = k - b * mass_ctas;
+  const int k = (int)(blockIdx.x - heads), b = k / mass_ctas, part = k - b * mass_ctas;
   const int len = checked_length(a.lengths, b, a.max_len);
   if (part * kMassChunk >= len) return;
-  for (int h = warp; h < a.Hq; h += kJoinThreads / 32) {
-    const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
-    const Span s = split_of(a, b, kvh * a.blocks + blk);
-    float z;
-    if (s.c0 == s.c1) {
-      z = a.lse2[(int64_t)b * a.Hq + h];
-    } else {
-      float m = -INFINITY, l = 0.f;
-      for (int c = s.c0 + lane; c <= s.c1; c += 32) {
-        const float2 ml = a.part_ml[part_slot(s, c) * a.heads + gi];
-        const float mn = fmaxf(m, ml.x);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        l = l * exp2f(m - base) + ml.y * exp2f(ml.x - base);
-        m = mn;
+  const int padded = (a.Hq + 7) & ~7;
+  for (int h0 = 0; h0 < padded; h0 += kJoinThreads / 4) {  // 4 lanes to a head
+    const int h = h0 + (threadIdx.x >> 2);
+    float m = -INFINITY, l = 0.f;
+    bool whole = false;
+    if (h < a.Hq) {
+      const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
+      const Span s = split_of(a, b, kvh * a.blocks + blk);
+      whole = s.c0 == s.c1;
+      if (whole) {
+        m = a.lse2[(int64_t)b * a.Hq + h];
+      } else {
+#pragma unroll 4
+        for (int c = s.c0 + (lane & 3); c <= s.c1; c += 4) {
+          const float2 ml = a.part_ml[part_slot(s, c) * a.heads + gi];
+          merge_ml(m, l, ml.x, ml.y);
+        }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        const float mn = fmaxf(m, m2);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        l = l * exp2f(m - base) + l2 * exp2f(m2 - base);
-        m = mn;
-      }
-      z = l > 0.f ? m + log2f(l) : -INFINITY;
     }
-    if (lane == 0) z2[h] = z;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+      if (!whole) merge_ml(m, l, m2, l2);
+    }
+    // a head without weights adds none: e^{s - inf} = 0
+    if ((lane & 3) == 0 && h < padded)
+      z2[h] = h >= a.Hq || m == -INFINITY ? INFINITY : whole ? m : m + log2f(l);
   }
   __syncthreads();
   const float inv = 1.f / (float)a.Hq;
+  const float* scores = a.scores + (int64_t)b * a.Hq * a.max_len;
   for (int j = part * kMassChunk + threadIdx.x; j < len; j += kMassChunk * mass_ctas) {
 #pragma unroll
     for (int half = 0; half < kMassChunk / kJoinThreads; ++half) {
       const int jj = j + half * kJoinThreads;
       if (jj >= len) break;
       float sum = 0.f;
-      for (int kvh = 0; kvh < a.c.Hkv; ++kvh) {
-        const float* sp = a.scores + (((int64_t)b * a.c.Hkv + kvh) * a.max_len + jj) * a.G;
-        for (int g = 0; g < a.G; ++g) {
-          const float z = z2[kvh * a.G + g];
-          if (z > -INFINITY) sum += exp2f(sp[g] - z);
-        }
+      for (int h = 0; h < a.Hq; h += 8) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = scores[(int64_t)min(h + e, a.Hq - 1) * a.max_len + jj];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += exp2f(x[e] - z2[h + e]);
       }
       const int64_t at = (int64_t)b * a.mass_stride + jj;
       const bool fresh = a.k_new && jj == len - 1;
@@ -908,18 +959,17 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   else
     err = c.d == 128 ? launch_simt<float, 128>(a, smem, stream) : launch_simt<float, 64>(a, smem, stream);
   if (err != cudaSuccess) return err;
-  // join: one warp per query head; masses: enough CTAs a sequence to fill the GPU a few times
-  const int out_ctas = (int)(((int64_t)p.B * p.Hq + 3) / 4);
+  // join: a CTA per query head; masses: enough CTAs a sequence to fill the GPU a few times
   int mass_ctas = 0;
   if (p.mass_out) {
     const int chunks = (p.max_len + kMassChunk - 1) / kMassChunk;
     const int fill = (device_info().sm_count * 8 + p.B - 1) / p.B;
     mass_ctas = chunks < fill ? chunks : fill;
   }
-  const dim3 grid(out_ctas + mass_ctas * p.B);
-  const size_t zmem = p.mass_out ? (size_t)p.Hq * 4 : 0;
+  const dim3 grid((unsigned)(p.B * p.Hq + mass_ctas * p.B));
+  const size_t zmem = p.mass_out ? ((size_t)p.Hq + 7) / 8 * 8 * 4 : 0;
   const auto join = [&](auto kernel) {
-    return launch_dependent(kernel, grid, dim3(kJoinThreads), zmem, stream, a, out_ctas, mass_ctas);
+    return launch_dependent(kernel, grid, dim3(kJoinThreads), zmem, stream, a, mass_ctas);
   };
   if (c.dtype == DD_BF16)
     return c.d == 128 ? join(paged_join_kernel<__nv_bfloat16, 128>)

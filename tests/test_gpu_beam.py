@@ -35,7 +35,7 @@ def _check(logits, score, done=None, eos=-1, gaps=True):
     for b in range(B):
         dn = None if done is None else done[b].cpu().numpy()
         if gaps:
-            best = OC.beam_candidates(x[b], score[b].cpu().numpy(), dn, eos, V)[:K + 1]
+            best = OC.beam_candidates(x[b], score[b].cpu().numpy(), dn, eos, V, K + 1)
             for (s, i), (s2, i2) in zip(best, best[1:]):
                 assert i // V == i2 // V or s2 - s > GAP
         parent, token, out, ended = OC.beam_select(x[b], score[b].cpu().numpy(), dn, eos)
