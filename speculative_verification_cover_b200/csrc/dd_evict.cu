@@ -6,7 +6,12 @@ namespace dd {
 
 namespace {
 
-constexpr int kEvictThreads = 512;
+// Threads of a CTA: for short sequences the barriers of fewer warps are cheaper.
+constexpr int kEvictFew = 256, kEvictMany = 1024;
+constexpr int kEvictRegs = 8;      // slots a thread holds from its first load
+constexpr int kEvictKeySlots = 45056;  // slots whose keys fit shared memory (176 KB)
+constexpr int kEvictBins = 2048;
+constexpr int kEvictList = 1024;   // keys of one bin ranked by counting
 
 // Ranking key of a slot: protected slots above everything, then the mass (as an
 // order-preserving integer; NaN below every number).
@@ -24,177 +29,309 @@ __device__ __forceinline__ uint32_t below_mask(int w, int limit) {
   return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
 
-// Exclusive prefix sum of f(w) over the words [w0, w1) into out[w].
+// Exclusive prefix sums of f(0) .. f(n - 1) into out; returns the total. out may be what f
+// reads.
 template <typename F>
-__device__ void scan_words(int w0, int w1, uint32_t* out, int* warp_tmp, F f) {
-  const int n = w1 - w0, chunk = (n + kEvictThreads - 1) / kEvictThreads;
-  const int a = w0 + min(n, (int)threadIdx.x * chunk), e = min(w1, a + chunk);
+__device__ int scan_block(int n, uint32_t* out, int* warp_tmp, F f) {
+  const int chunk = (n + blockDim.x - 1) / blockDim.x;
+  const int a = min(n, (int)threadIdx.x * chunk), e = min(n, a + chunk);
   int sum = 0;
   for (int w = a; w < e; ++w) sum += f(w);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  __syncthreads();
   if (lane == 31) warp_tmp[warp] = incl;
   __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < warp; ++w) run += warp_tmp[w];
+  int x = lane < warps ? warp_tmp[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
+  }
+  const int total = __shfl_sync(0xffffffffu, x, 31);
+  const int before = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0);
+  int run = incl - sum + (warp > 0 ? before : 0);
   for (int w = a; w < e; ++w) {
-    const int c = f(w);  // before out[w] is written: out may be what f reads
+    const int c = f(w);
     out[w] = (uint32_t)run;
     run += c;
   }
   __syncthreads();
+  return total;
 }
 
 // Grid (CTAs per sequence, sequences). The selection reads 8 bytes a slot; every CTA of a
 // sequence repeats it (the repeats come from L2) and then does its share of the moves, so
-// nothing has to be handed from one CTA to another. The budget-th largest key is found by
-// a radix select, 8 bits a pass; kept slots become a bitmap in shared memory, and the i-th
-// freed slot below the new length takes the i-th kept slot at or beyond it: both are ranks
-// over the bitmap (a prefix count per word and a bit count).
-__global__ void __launch_bounds__(kEvictThreads)
+// nothing has to be handed from one CTA to another.
+// The budget-th largest key is found by histograms of 11 bits; the first leaves, with
+// attention masses, a bin of few keys, which are ranked by counting (a bin of more than
+// kEvictList keys gets another histogram). Kept slots become a bitmap, and the i-th freed
+// slot below the new length takes the i-th kept slot at or beyond it: both are ranks over
+// the bitmap (one prefix count per word and a bit count).
+__global__ void __launch_bounds__(kEvictMany)
 evict_kernel(PagedView c, const int32_t* __restrict__ lengths, int max_len, int budget, int sink,
              int recent, const float* __restrict__ mass_in, const int32_t* __restrict__ pos_in,
              int64_t stride, float* __restrict__ mass_out, int32_t* __restrict__ pos_out,
-             int32_t* __restrict__ src_out, int32_t* __restrict__ lengths_out, int chunk16_log2) {
+             int32_t* __restrict__ src_out, int32_t* __restrict__ lengths_out, int chunk16_log2,
+             bool keys_fit) {
   extern __shared__ uint32_t words[];
-  __shared__ unsigned int hist[256];
-  __shared__ int warp_tmp[kEvictThreads / 32];
+  __shared__ int hist[kEvictBins];
+  __shared__ uint32_t list[kEvictList];
+  __shared__ int warp_tmp[32];
   __shared__ uint32_t prefix_s;
-  __shared__ int need_s, newest_s, moves_s;
-  __shared__ int2 moves[kEvictThreads];
+  __shared__ int want_s, ties_s, newest_s, n_s;
+  __shared__ int64_t s_to[kEvictMany], s_from[kEvictMany];
   const int n = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int threads = blockDim.x;
   const int len = checked_length(lengths, n, max_len);
   const int left = min(len, budget);
   const float* mass = mass_in + (int64_t)n * stride;
   const int32_t* pos = pos_in + (int64_t)n * stride;
   if (blockIdx.x == 0 && threadIdx.x == 0) lengths_out[n] = left;
   const int W = (len + 31) >> 5, wl = left >> 5;
-  uint32_t* kept = words;         // [W] bitmap
-  uint32_t* rank = words + W;     // [W] freed slots before word w (w <= wl), else movers before it
-  uint32_t* tie = words + 2 * W;  // [W] bitmap of slots at the threshold
+  uint32_t* kept = words;          // [W] bitmap
+  uint32_t* rank = words + W;      // [W] freed slots and movers before word w
+  uint32_t* tie = words + 2 * W;   // [W] bitmap of slots at the threshold
+  uint32_t* keys = words + 3 * W;  // [len], where they fit
+  int moves_total = 0;
   if (len > budget) {
+    // ---- keys
     if (threadIdx.x == 0) newest_s = INT32_MIN;
-    for (int t = threadIdx.x; t < 256; t += kEvictThreads) hist[t] = 0u;
+    for (int t = threadIdx.x; t < kEvictBins; t += threads) hist[t] = 0;
+    float m[kEvictRegs];
+    int p[kEvictRegs];
+    const auto load = [&](int base) {
+#pragma unroll
+      for (int e = 0; e < kEvictRegs; ++e) {
+        const int j = base + e * threads + threadIdx.x;
+        m[e] = j < len ? mass[j] : 0.f;
+        p[e] = j < len ? pos[j] : INT32_MIN;
+      }
+    };
+    const int step = kEvictRegs * threads;
+    load(0);
+    int top = p[0];
+#pragma unroll
+    for (int e = 1; e < kEvictRegs; ++e) top = max(top, p[e]);
+    for (int base = step; base < len; base += step) {
+      int q[kEvictRegs];
+#pragma unroll
+      for (int e = 0; e < kEvictRegs; ++e) {
+        const int j = base + e * threads + threadIdx.x;
+        q[e] = j < len ? pos[j] : INT32_MIN;
+      }
+#pragma unroll
+      for (int e = 0; e < kEvictRegs; ++e) top = max(top, q[e]);
+    }
     __syncthreads();
-    int top = INT32_MIN;
-    for (int j = threadIdx.x; j < len; j += kEvictThreads) top = max(top, pos[j]);
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) atomicMax(&newest_s, top);
     __syncthreads();
     const int64_t newest = newest_s;
-    uint32_t prefix = 0u;
-    int want = budget;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      const uint32_t hmask = shift == 24 ? 0u : (0xFFFFFFFFu << (shift + 8));
-      for (int j = threadIdx.x; j < len; j += kEvictThreads) {
-        const uint32_t key = evict_key(mass[j], pos[j], sink, newest, recent);
-        if ((key & hmask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        unsigned int cnt[8], sum = 0;
+    const auto key_at = [&](int j) {
+      return keys_fit ? keys[j] : evict_key(mass[j], pos[j], sink, newest, recent);
+    };
+    // first histogram (the top 11 bits) as the keys are formed
+    int safe = 0;
+    for (int base = 0; base < len; base += step) {
+      if (base > 0) load(base);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) { cnt[e] = hist[255 - 8 * lane - e]; sum += cnt[e]; }
-        unsigned int incl = sum;
+      for (int e = 0; e < kEvictRegs; ++e) {
+        const int j = base + e * threads + threadIdx.x;
+        if (j >= len) continue;
+        const uint32_t key = evict_key(m[e], p[e], sink, newest, recent);
+        if (keys_fit) keys[j] = key;
+        if (key == 0xFFFFFFFFu) ++safe;
+        else atomicAdd(&hist[key >> 21], 1);
+      }
+    }
+    safe = __reduce_add_sync(0xffffffffu, safe);
+    if (lane == 0 && safe) atomicAdd(&hist[kEvictBins - 1], safe);
+    __syncthreads();
+    uint32_t prefix = 0u;  // bits of the threshold found so far
+    int want = budget, bits = 21;
+    while (true) {
+      // the bin, from the top, that the want-th largest key falls into
+      const int bins = bits == 21 || bits == 10 ? kEvictBins : 1024;
+      int count = 0;
+      {
+        // thread t holds bins from the top: bins - 1 - t * per ...
+        const int per = (bins + threads - 1) / threads;
+        const int b0 = (int)threadIdx.x * per, b1 = min(bins, b0 + per);
+        int sum = 0;
+        for (int x = b0; x < b1; ++x) sum += hist[bins - 1 - x];
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const unsigned int t = __shfl_up_sync(0xffffffffu, incl, o);
+          const int t = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += t;
         }
-        unsigned int run = incl - sum;
+        if (lane == 31) warp_tmp[warp] = incl;
+        __syncthreads();
+        int x = lane < (threads >> 5) ? warp_tmp[lane] : 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (run < (unsigned)want && run + cnt[e] >= (unsigned)want) {
-            prefix_s = prefix | ((uint32_t)(255 - 8 * lane - e) << shift);
-            need_s = want - (int)run;
-          }
-          run += cnt[e];
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += t;
         }
+        const int before = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0);
+        int run = incl - sum + (warp > 0 ? before : 0);
+        if (run < want && run + sum >= want)
+          for (int y = b0; y < b1; ++y) {
+            const int h = hist[bins - 1 - y];
+            if (run < want && run + h >= want) {
+              prefix_s = prefix | ((uint32_t)(bins - 1 - y) << bits);
+              want_s = want - run;
+              ties_s = h;
+            }
+            run += h;
+          }
+        if (threadIdx.x == 0) n_s = 0;
+        __syncthreads();
+        prefix = prefix_s;
+        want = want_s;
+        count = ties_s;
       }
+      const uint32_t mask = bits == 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << bits;
+      if (bits == 0 || count <= kEvictList) {
+        if (bits > 0) {  // rank the bin's keys
+          for (int j = threadIdx.x; j < len; j += threads) {
+            const uint32_t key = key_at(j);
+            if ((key & mask) == prefix) {
+              const int at = atomicAdd(&n_s, 1);
+              if (DD_IN_BOUNDS(at < kEvictList)) list[at] = key;
+            }
+          }
+          __syncthreads();
+          for (int i = threadIdx.x; i < count; i += threads) {
+            const uint32_t key = list[i];
+            int above = 0, equal = 0;
+            for (int t = 0; t < count; ++t) {
+              above += list[t] > key;
+              equal += list[t] == key;
+            }
+            if (above < want && above + equal >= want) {  // the same from each equal key
+              prefix_s = key;
+              want_s = want - above;
+              ties_s = equal;
+            }
+          }
+          __syncthreads();
+          prefix = prefix_s;
+          want = want_s;
+        }
+        break;
+      }
+      // another 11 (then 10) bits
+      const int next = bits == 21 ? 10 : 0;
+      for (int t = threadIdx.x; t < kEvictBins; t += threads) hist[t] = 0;
       __syncthreads();
-      prefix = prefix_s;
-      want = need_s;
-      for (int t = threadIdx.x; t < 256; t += kEvictThreads) hist[t] = 0u;
+      for (int j = threadIdx.x; j < len; j += threads) {
+        const uint32_t key = key_at(j);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> next) & (next == 10 ? 2047u : 1023u)], 1);
+      }
+      bits = next;
       __syncthreads();
     }
-    // kept: above the threshold, and the `want` lowest of the slots at it
-    for (int w = warp; w < W; w += kEvictThreads / 32) {
+    const bool all_ties = ties_s == want;
+    // ---- kept: above the threshold, and the `want` lowest of the slots at it
+    for (int w = warp; w < W; w += threads >> 5) {
       const int j = w * 32 + lane;
-      const uint32_t key = j < len ? evict_key(mass[j], pos[j], sink, newest, recent) : 0u;
+      const uint32_t key = j < len ? key_at(j) : 0u;
       const uint32_t gt = __ballot_sync(0xffffffffu, j < len && key > prefix);
       const uint32_t eq = __ballot_sync(0xffffffffu, j < len && key == prefix);
-      if (lane == 0) { kept[w] = gt; tie[w] = eq; }
-    }
-    __syncthreads();
-    scan_words(0, W, rank, warp_tmp, [&](int w) { return __popc(tie[w]); });
-    for (int w = threadIdx.x; w < W; w += kEvictThreads) {
-      uint32_t bits = tie[w], take = 0u;
-      for (int left_over = want - (int)rank[w]; left_over > 0 && bits; --left_over) {
-        take |= bits & (0u - bits);
-        bits &= bits - 1u;
+      if (lane == 0) {
+        kept[w] = all_ties ? gt | eq : gt;
+        tie[w] = eq;
       }
-      kept[w] |= take;
     }
     __syncthreads();
-    scan_words(0, wl + 1 < W ? wl + 1 : W, rank, warp_tmp,
-               [&](int w) { return __popc(~kept[w] & below_mask(w, left)); });
-    const uint32_t first = wl < W ? kept[wl] & ~below_mask(wl, left) : 0u;  // movers of the word `left` is in
-    scan_words(wl + 1 < W ? wl + 1 : W, W, rank, warp_tmp, [&](int w) { return __popc(kept[w]); });
-    for (int w = wl + 1 + threadIdx.x; w < W; w += kEvictThreads) rank[w] += __popc(first);
-    __syncthreads();
+    if (!all_ties) {
+      scan_block(W, rank, warp_tmp, [&](int w) { return __popc(tie[w]); });
+      for (int w = threadIdx.x; w < W; w += threads) {
+        uint32_t from = tie[w], take = 0u;
+        for (int more = want - (int)rank[w]; more > 0 && from; --more) {
+          take |= from & (0u - from);
+          from &= from - 1u;
+        }
+        kept[w] |= take;
+      }
+      __syncthreads();
+    }
+    // freed slots lie below `left`, movers at or beyond it; there are as many of each
+    moves_total = scan_block(W, rank, warp_tmp, [&](int w) {
+      const uint32_t b = below_mask(w, left);
+      return __popc((~kept[w] & b) | (kept[w] & ~b));
+    }) / 2;
   }
   // ---- this CTA's share of the new slots
-  for (int base = blockIdx.x * kEvictThreads; base < left; base += gridDim.x * kEvictThreads) {
-    if (threadIdx.x == 0) moves_s = 0;
+  const int share = ((left + gridDim.x - 1) / gridDim.x + 31) & ~31;
+  const int end = min(left, (int)(blockIdx.x + 1) * share);
+  const int32_t* row = c.table + (int64_t)n * c.table_stride;
+  const int per = c.Hkv << chunk16_log2;  // 16-byte chunks of a row
+  const int64_t at = (int64_t)n * stride;
+  for (int base = blockIdx.x * share; base < end; base += threads) {
+    if (threadIdx.x == 0) n_s = 0;
     __syncthreads();
     const int j = base + threadIdx.x;
-    if (j < left) {
+    if (j < end) {
       int src = j;
-      if (len > budget) {
+      if (moves_total > 0) {
         const int w = j >> 5;
         if (!((kept[w] >> (j & 31)) & 1u)) {
-          int r = (int)rank[w] + __popc(~kept[w] & below_mask(w, j));  // this freed slot's rank
-          int lo = wl, hi = W - 1;  // the last word with at most r movers before it
+          // this freed slot's rank among them, and the mover of the same rank: the last word
+          // with at most that many movers before it
+          int r = (int)rank[w] + __popc(~kept[w] & below_mask(w, j));
+          int lo = wl, hi = W - 1;
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if ((int)rank[mid] <= r) lo = mid; else hi = mid - 1;
+            if ((int)rank[mid] - moves_total <= r) lo = mid; else hi = mid - 1;
           }
-          uint32_t bits = kept[lo] & ~below_mask(lo, left);
-          if (lo > wl) r -= (int)rank[lo];
-          for (; r > 0; --r) bits &= bits - 1u;
-          src = lo * 32 + __ffs(bits) - 1;
-          if (DD_IN_BOUNDS(bits != 0u && src < len)) {
-            moves[atomicAdd(&moves_s, 1)] = make_int2(j, src);
-          } else {
-            src = j;
+          uint32_t b = kept[lo] & ~below_mask(lo, left);
+          if (lo > wl) r -= (int)rank[lo] - moves_total;
+          for (; r > 0; --r) b &= b - 1u;
+          const int from = lo * 32 + __ffs(b) - 1;
+          if (DD_IN_BOUNDS(b != 0u && from < len)) {
+            src = from;
+            const int64_t ot = slot_offset(c, row, j), of = slot_offset(c, row, src);
+            if (ot >= 0 && of >= 0) {
+              const int i = atomicAdd(&n_s, 1);
+              s_to[i] = ot;
+              s_from[i] = of;
+            }
           }
         }
       }
-      const int64_t at = (int64_t)n * stride;
       mass_out[at + j] = mass[src];
       pos_out[at + j] = pos[src];
       if (src_out) src_out[at + j] = src;
     }
     __syncthreads();
-    const int n_moves = moves_s;
-    const int32_t* row = c.table + (int64_t)n * c.table_stride;
-    const int per = c.Hkv << chunk16_log2;  // 16-byte chunks of a row
-    for (int i = warp; i < n_moves; i += kEvictThreads / 32) {
-      const int64_t to = slot_offset(c, row, moves[i].x), from = slot_offset(c, row, moves[i].y);
-      if (to < 0 || from < 0) continue;
-      for (int x = lane; x < per; x += 32) {
-        const int64_t off = (int64_t)(x >> chunk16_log2) * c.head_bytes +
-                            (int64_t)(x & ((1 << chunk16_log2) - 1)) * 16;
-        const uint4 kx = *reinterpret_cast<const uint4*>(c.k + from + off);
-        const uint4 vx = *reinterpret_cast<const uint4*>(c.v + from + off);
-        *reinterpret_cast<uint4*>(c.k + to + off) = kx;
-        *reinterpret_cast<uint4*>(c.v + to + off) = vx;
+    // rows that move: K and V, 16 bytes a thread and step
+    const int units = n_s * per;
+    for (int u = threadIdx.x; u < units; u += 4 * threads) {
+      uint4 kx[4], vx[4];
+      int64_t to[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int x = u + e * threads;
+        if (x >= units) continue;
+        const int i = x / per, y = x - i * per;
+        const int64_t off = (int64_t)(y >> chunk16_log2) * c.head_bytes +
+                            (int64_t)(y & ((1 << chunk16_log2) - 1)) * 16;
+        kx[e] = *reinterpret_cast<const uint4*>(c.k + s_from[i] + off);
+        vx[e] = *reinterpret_cast<const uint4*>(c.v + s_from[i] + off);
+        to[e] = s_to[i] + off;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (u + e * threads >= units) continue;
+        *reinterpret_cast<uint4*>(c.k + to[e]) = kx[e];
+        *reinterpret_cast<uint4*>(c.v + to[e]) = vx[e];
       }
     }
     __syncthreads();
@@ -297,19 +434,27 @@ int chunk_log2(const dd_paged_cache& c) {  // log2 of the 16-byte chunks of a he
 cudaError_t launch_cache_evict(const EvictCall& p, cudaStream_t stream) {
   static thread_local int configured_for = -1;
   const DeviceInfo& dev = device_info();
+  constexpr int kBitmaps = kEvictMaxLen / 32 * 3 * 4;
+  constexpr int kWithKeys = kEvictKeySlots * 4 + (kEvictKeySlots + 31) / 32 * 3 * 4;
   if (configured_for != dev.device) {
     cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kEvictMaxLen / 32 * 3 * (int)sizeof(uint32_t));
+                                         kBitmaps > kWithKeys ? kBitmaps : kWithKeys);
     if (e != cudaSuccess) return e;
     configured_for = dev.device;
   }
+  const int threads = p.max_len <= kEvictFew * kEvictRegs ? kEvictFew : kEvictMany;
+  const bool keys_fit = p.max_len <= kEvictKeySlots;
+  const size_t smem = (size_t)((p.max_len + 31) / 32) * 3 * 4 + (keys_fit ? (size_t)p.max_len * 4 : 0);
+  // CTAs per sequence: one per 32 rows that may move, and per 8192 slots that stay, until
+  // the GPU is full
   const int most = p.budget < p.max_len ? p.budget : p.max_len;
-  const int parts = (most + kEvictThreads - 1) / kEvictThreads;
+  const int movers = most < p.max_len - most ? most : p.max_len - most;
+  const int parts = (movers + 31) / 32 > (most + 8191) / 8192 ? (movers + 31) / 32 : (most + 8191) / 8192;
   const int fill = (2 * dev.sm_count + p.N - 1) / p.N;
-  const size_t smem = (size_t)((p.max_len + 31) / 32) * 3 * sizeof(uint32_t);
-  evict_kernel<<<dim3(parts < fill ? parts : fill, p.N), kEvictThreads, smem, stream>>>(
+  evict_kernel<<<dim3(parts < fill ? parts : fill, p.N), threads, smem, stream>>>(
       make_paged_view(*p.cache), p.lengths, p.max_len, p.budget, p.sink, p.recent, p.mass_in,
-      p.pos_in, p.stride, p.mass_out, p.pos_out, p.src_out, p.lengths_out, chunk_log2(*p.cache));
+      p.pos_in, p.stride, p.mass_out, p.pos_out, p.src_out, p.lengths_out, chunk_log2(*p.cache),
+      keys_fit);
   return cudaGetLastError();
 }
 

@@ -366,72 +366,85 @@ def dd_decide(policy, tokens, is_seed, eligible, stats: RowStats, pos_offset, de
 # ------------------------------------------------------------------ cached decoding
 # Every tensor of a call is checked here -- device, type, shape, layout -- before its
 # address reaches the library; the call runs on that device, on `stream` (None: its
-# current stream), and a workspace that is not given is allocated for that stream.
-def _dev(t, name):
+# current stream), and a workspace that is not given is allocated for that stream. A
+# decode step makes many small calls, so the checks are one expression a tensor, and what
+# is wrong is looked for only once something is.
+def _gpu(t, name):
+    """Index of the device a call runs on: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"libdd takes device memory: {name} is on the CPU")
-    return t.device
+    return t.get_device()
 
 
-def _arg(t, name, dtype, shape, device, packed=True):
-    """Address of a tensor of the given type, shape and device. packed: contiguous;
-    otherwise only rows (all dimensions but the first) must be."""
+def _refuse(t, name, dtype, shape, gpu, rows):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{gpu}")
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    if not (t.is_contiguous() if packed or t.shape[0] < 2 else t[0].is_contiguous()):
-        raise ValueError(f"{name} must be contiguous" + ("" if packed else " within a row"))
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous" + (" within a row" if rows else ""))
 
 
-def _opt(t, *args, **kw):
-    return None if t is None else _arg(t, *args, **kw)
+def _arg(t, name, dtype, shape, gpu):
+    """Address of a contiguous tensor of the given type, shape and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, gpu, False)
 
 
-def _row_stride(t):
-    """Elements from row to row (0 where there is one row)."""
-    return t.stride(0) if t.shape[0] > 1 else 0
+def _rows(t, name, dtype, shape, gpu):
+    """Address and row stride of a tensor whose rows (all dimensions but the first) are
+    contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == gpu:
+            if t.is_contiguous() or (t.shape[0] > 1 and t[0].is_contiguous()):
+                return t.data_ptr(), t.stride(0)
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, gpu, True)
 
 
-class _On:
-    """Makes `device` current for a call (a change of device only where one is needed)."""
-
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
-
-
-def _scratch(nbytes, device, stream):
+def _scratch(nbytes, gpu, stream):
     """Device scratch that the allocator reuses in the order of `stream`."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{gpu}")
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), f"cuda:{gpu}")
     with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{gpu}")
 
 
-def _workspace(workspace, nbytes, device, stream):
-    if workspace is None:
-        return _scratch(nbytes, device, stream)
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on {device}")
-    if not workspace.is_contiguous():
+def _workspace(t, gpu):
+    """Address and bytes of a caller's workspace."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
+    if t.get_device() != gpu:
+        raise ValueError(f"workspace is on {t.device}, the call's other tensors on cuda:{gpu}")
+    if not t.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _call(name, gpu, stream, *args):
+    """A library call on device `gpu` (made current only where it is not), on `stream`."""
+    fn = getattr(lib(), name)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(gpu)
+    else:
+        s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == gpu:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(gpu):
+            st = fn(*args, s)
+    if st != DD_OK:
+        raise DDError(name, st)
 
 
 class PagedCache:
@@ -441,8 +454,8 @@ class PagedCache:
     stored heads first is passed as its transposed view). A page id below 0 is a hole."""
 
     def __init__(self, k, v, page_table):
-        dev = _dev(k, "k")
-        if _dev(v, "v") != dev or _dev(page_table, "page_table") != dev:
+        gpu = _gpu(k, "k")
+        if _gpu(v, "v") != gpu or _gpu(page_table, "page_table") != gpu:
             raise ValueError("k, v and page_table must be on one device")
         if k.dim() not in (4, 5) or v.shape != k.shape or v.stride() != k.stride():
             raise ValueError("k and v must be [pages, page_size, Hkv, d] or [layers, pages, "
@@ -457,20 +470,17 @@ class PagedCache:
             raise ValueError("page_table must be a non-empty [N, max_pages] int32 tensor")
         if page_table.stride(1) != 1 and page_table.shape[1] > 1:
             raise ValueError("page_table must be contiguous within a row")
-        self.k, self.v, self.page_table, self.device, self.dtype = k, v, page_table, dev, k.dtype
+        self.k, self.v, self.page_table, self.gpu, self.dtype = k, v, page_table, gpu, k.dtype
         *layers, self.n_pages, self.page_size, self.Hkv, self.d = k.shape
         self.layers = layers[0] if layers else 1
         self.N, self.max_pages = page_table.shape
+        self.slots = self.max_pages * self.page_size  # what a table row has room for
         s = [st if n > 1 else 0 for n, st in zip(k.shape, k.stride())]
         self._c = _PagedCache(k.data_ptr(), v.data_ptr(), s[0] if layers else 0, *s[-4:-1],
                               self.layers, self.n_pages, self.page_size, self.Hkv, self.d,
                               _dtype_code(k), page_table.data_ptr(),
                               page_table.stride(0) if self.N > 1 else self.max_pages, self.max_pages)
-
-    @property
-    def slots(self):
-        """Slots a table row has room for."""
-        return self.max_pages * self.page_size
+        self._ref = ctypes.byref(self._c)
 
     def layer(self, i):
         """One layer's cache of a several-layer one (the same memory and page table)."""
@@ -482,12 +492,11 @@ class PagedCache:
         """The same pools under another page table (dd_paged_fork's, say)."""
         return PagedCache(self.k, self.v, page_table)
 
-    def _sequences(self, n):
+    def _fits(self, n, gpu):
         if n != self.N:
             raise ValueError(f"the page table has {self.N} rows, the call {n} sequences")
-
-    def _ref(self):
-        return ctypes.byref(self._c)
+        if gpu != self.gpu:
+            raise ValueError(f"the cache is on cuda:{self.gpu}, the call's tensors on cuda:{gpu}")
 
 
 def dd_paged_attention_workspace_size(B, Hq, Hkv, d, max_len, with_mass=False) -> int:
@@ -502,43 +511,48 @@ def dd_paged_attention(q, cache: PagedCache, lengths, out, lse=None, k_new=None,
     k_new, v_new [B,Hkv,d]: appended at slot lengths - 1 first; mass (None: zero),
     mass_out [B,M] fp32 with M >= max_len: the attention mass per slot, added up. max_len:
     bound on lengths (None: the smaller of M and what the page table has room for)."""
-    dev = _dev(q, "q")
+    gpu = _gpu(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    cache._sequences(B)
-    if d != cache.d or Hq % cache.Hkv:
-        raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.Hkv} heads of {cache.d}")
-    if cache.device != dev:
-        raise ValueError(f"q is on {dev}, the cache on {cache.device}")
-    if max_len is None:
-        max_len = cache.slots if mass_out is None else min(cache.slots, mass_out.shape[-1])
-    new = (B, cache.Hkv, d)
-    f32 = torch.float32
-    if mass_out is None and mass is not None:
+    shape = q.shape
+    B, Hq, d = shape
+    Hkv, dtype = cache.Hkv, cache.dtype
+    cache._fits(B, gpu)
+    if d != cache.d or Hq % Hkv:
+        raise ValueError(f"q {tuple(shape)} does not fit a cache of {Hkv} heads of {cache.d}")
+    qp, qs = _rows(q, "q", dtype, shape, gpu)
+    op = _arg(out, "out", dtype, shape, gpu)
+    np_ = _arg(lengths, "lengths", torch.int32, (B,), gpu)
+    lp = None if lse is None else _arg(lse, "lse", torch.float32, (B, Hq), gpu)
+    kp = vp = None
+    ns = 0
+    if k_new is not None or v_new is not None:
+        kp, ns = _rows(k_new, "k_new", dtype, (B, Hkv, d), gpu)
+        vp, vs = _rows(v_new, "v_new", dtype, (B, Hkv, d), gpu)
+        if ns != vs and B > 1:
+            raise ValueError("k_new and v_new must have the same strides")
+    mi = mo = None
+    ms = 0
+    if mass_out is not None:
+        rows = (B, mass_out.shape[-1])
+        mo, ms = _rows(mass_out, "mass_out", torch.float32, rows, gpu)
+        if mass is not None:
+            mi, vs = _rows(mass, "mass", torch.float32, rows, gpu)
+            if ms != vs and B > 1:
+                raise ValueError("mass and mass_out must have the same strides")
+        if B == 1:
+            ms = rows[1]
+        if max_len is None:
+            max_len = min(cache.slots, rows[1])
+    elif mass is not None:
         raise ValueError("mass without mass_out")
-    rows = None if mass_out is None else (B, mass_out.shape[-1])
-    if mass is not None and mass.stride() != mass_out.stride():
-        raise ValueError("mass and mass_out must have the same strides")
-    qp = _arg(q, "q", cache.dtype, (B, Hq, d), dev, packed=False)
-    kp, vp = (_opt(t, n, cache.dtype, new, dev, packed=False)
-              for t, n in ((k_new, "k_new"), (v_new, "v_new")))
-    if k_new is not None and v_new is not None and _row_stride(k_new) != _row_stride(v_new):
-        raise ValueError("k_new and v_new must have the same strides")
-    op = _arg(out, "out", cache.dtype, (B, Hq, d), dev)
-    args = (_arg(lengths, "lengths", torch.int32, (B,), dev),)
-    lp = _opt(lse, "lse", f32, (B, Hq), dev)
-    mi = _opt(mass, "mass", f32, rows, dev, packed=False)
-    mo = _opt(mass_out, "mass_out", f32, rows, dev, packed=False)
-    stride = 0 if mass_out is None else mass_out.stride(0) if B > 1 else mass_out.shape[1]
-    with _On(dev):
-        ws = _workspace(workspace, 0 if workspace is not None else dd_paged_attention_workspace_size(
-            B, Hq, cache.Hkv, d, int(max_len), mass_out is not None), dev, stream)
-        st = lib().dd_paged_attention(
-            qp, _row_stride(q), kp, vp, 0 if k_new is None else _row_stride(k_new), cache._ref(),
-            *args, B, Hq, int(max_len), float(softmax_scale), op, lp, mi, mo, stride,
-            ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
-    _check("dd_paged_attention", st)
+    max_len = cache.slots if max_len is None else int(max_len)
+    if workspace is None:
+        workspace = _scratch(dd_paged_attention_workspace_size(B, Hq, Hkv, d, max_len, mo is not None), gpu,
+                             stream)
+    wp, wb = _workspace(workspace, gpu)
+    _call("dd_paged_attention", gpu, stream, qp, qs, kp, vp, ns, cache._ref, np_, B, Hq, max_len,
+          softmax_scale, op, lp, mi, mo, ms, wp, wb)
 
 
 def dd_cache_evict(cache: PagedCache, lengths, mass, pos, budget, mass_out, pos_out, lengths_out,
@@ -547,24 +561,23 @@ def dd_cache_evict(cache: PagedCache, lengths, mass, pos, budget, mass_out, pos_
     [N,M] fp32, pos, pos_out, src (optional output: each new slot's old one) [N,M] int32,
     M >= max_len; lengths, lengths_out [N] int32; outputs are other tensors than inputs.
     max_len: bound on lengths (None: the smaller of M and what the page table has room for)."""
-    dev = _dev(mass, "mass")
+    gpu = _gpu(mass, "mass")
     if mass.dim() != 2:
         raise ValueError("mass must be [N, M]")
-    N, M = mass.shape
-    cache._sequences(N)
-    if cache.device != dev:
-        raise ValueError(f"mass is on {dev}, the cache on {cache.device}")
+    shape = mass.shape
+    N, M = shape
+    cache._fits(N, gpu)
     max_len = min(M, cache.slots) if max_len is None else int(max_len)
     i32, f32 = torch.int32, torch.float32
-    ptr = [_arg(t, n, dt, (N, M), dev) for t, n, dt in
-           ((mass, "mass", f32), (pos, "pos", i32), (mass_out, "mass_out", f32),
-            (pos_out, "pos_out", i32))]
-    sp = _opt(src, "src", i32, (N, M), dev)
-    ln, lo = (_arg(t, n, i32, (N,), dev) for t, n in ((lengths, "lengths"), (lengths_out, "lengths_out")))
-    with _On(dev):
-        st = lib().dd_cache_evict(cache._ref(), ln, N, max_len, int(budget), int(sink), int(recent),
-                                  ptr[0], ptr[1], M, ptr[2], ptr[3], sp, lo, _stream(stream))
-    _check("dd_cache_evict", st)
+    mi = _arg(mass, "mass", f32, shape, gpu)
+    pi = _arg(pos, "pos", i32, shape, gpu)
+    mo = _arg(mass_out, "mass_out", f32, shape, gpu)
+    po = _arg(pos_out, "pos_out", i32, shape, gpu)
+    sp = None if src is None else _arg(src, "src", i32, shape, gpu)
+    ln = _arg(lengths, "lengths", i32, (N,), gpu)
+    lo = _arg(lengths_out, "lengths_out", i32, (N,), gpu)
+    _call("dd_cache_evict", gpu, stream, cache._ref, ln, N, max_len, int(budget), int(sink), int(recent),
+          mi, pi, M, mo, po, sp, lo)
 
 
 def dd_beam_select_workspace_size(B, K, V, dtype) -> int:
@@ -577,49 +590,54 @@ def dd_beam_select(logits, score, parent, token, score_out, done=None, done_out=
     """One step of beam search: logits [B,K,V] (a view narrowed from a wider [B,K,ld] buffer is
     accepted), score, score_out [B,K] fp32, parent, token [B,K] int32, done, done_out [B,K]
     uint8. Outputs are other tensors than inputs."""
-    dev = _dev(logits, "logits")
+    gpu = _gpu(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits must be [B, K, V]")
     B, K, V = logits.shape
-    ld = logits.stride(1) if K > 1 else logits.stride(0) if B > 1 else -(-V // 8) * 8
-    if (V > 1 and logits.stride(2) != 1) or (B > 1 and logits.stride(0) != K * ld):
+    per_b, ld, unit = logits.stride()
+    if K == 1:
+        ld = per_b if B > 1 else -(-V // 8) * 8
+    if (V > 1 and unit != 1) or (B > 1 and per_b != K * ld):
         raise ValueError("logits must be [B,K,V] with unit vocabulary stride and packed rows")
     i32, f32, bk = torch.int32, torch.float32, (B, K)
-    sp, so = (_arg(t, n, f32, bk, dev) for t, n in ((score, "score"), (score_out, "score_out")))
-    pp, tp = (_arg(t, n, i32, bk, dev) for t, n in ((parent, "parent"), (token, "token")))
-    dp, do = (_opt(t, n, torch.uint8, bk, dev) for t, n in ((done, "done"), (done_out, "done_out")))
+    sp = _arg(score, "score", f32, bk, gpu)
+    so = _arg(score_out, "score_out", f32, bk, gpu)
+    pp = _arg(parent, "parent", i32, bk, gpu)
+    tp = _arg(token, "token", i32, bk, gpu)
+    dp = None if done is None else _arg(done, "done", torch.uint8, bk, gpu)
+    do = None if done_out is None else _arg(done_out, "done_out", torch.uint8, bk, gpu)
     code = _dtype_code(logits)
-    with _On(dev):
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        lib().dd_beam_select_workspace_size(B, K, V, code), dev, stream)
-        st = lib().dd_beam_select(logits.data_ptr(), code, B, K, V, ld, sp, dp, int(eos), pp, tp, so,
-                                  do, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
-    _check("dd_beam_select", st)
+    if workspace is None:
+        workspace = _scratch(lib().dd_beam_select_workspace_size(B, K, V, code), gpu, stream)
+    wp, wb = _workspace(workspace, gpu)
+    _call("dd_beam_select", gpu, stream, logits.data_ptr(), code, B, K, V, ld, sp, dp, int(eos), pp, tp, so,
+          do, wp, wb)
+
+
+_ROW_STATES = [_RowState * max(1, n) for n in range(17)]
 
 
 def dd_beam_reorder(parent, states, stream=None):
     """States follow their parents: parent [B,K] int32; states: up to 8 pairs (src, dst) of
     tensors [B*K, ...] or [B,K,...], contiguous, of the same shape and dtype."""
-    dev = _dev(parent, "parent")
+    gpu = _gpu(parent, "parent")
     if parent.dim() != 2:
         raise ValueError("parent must be [B, K]")
     B, K = parent.shape
     n = B * K
-    c = (_RowState * max(1, len(states)))()
-    for i, (src, dst) in enumerate(states):
-        sp = _arg(src, "src", src.dtype, src.shape, dev)
-        dp = _arg(dst, "dst", src.dtype, src.shape, dev)
-        if src.shape[0] != n and src.shape[:2] != (B, K):
-            raise ValueError(f"a state must be [B*K, ...] or [B, K, ...], got {tuple(src.shape)}")
+    c = _ROW_STATES[min(len(states), 16)]()
+    for x, (src, dst) in zip(c, states):
+        shape = src.shape
+        sp = _arg(src, "src", src.dtype, shape, gpu)
+        dp = _arg(dst, "dst", src.dtype, shape, gpu)
+        if shape[0] != n and shape[:2] != (B, K):
+            raise ValueError(f"a state must be [B*K, ...] or [B, K, ...], got {tuple(shape)}")
         size = src.numel() * src.element_size()
-        row = size // n
         if sp < dp + size and dp < sp + size:
             raise ValueError("src and dst of a state must not overlap")
-        c[i] = _RowState(sp, dp, row, row, row)
-    pp = _arg(parent, "parent", torch.int32, (B, K), dev)
-    with _On(dev):
-        st = lib().dd_beam_reorder(pp, B, K, c, len(states), _stream(stream))
-    _check("dd_beam_reorder", st)
+        x.src, x.dst = sp, dp
+        x.row_bytes = x.src_stride = x.dst_stride = size // n
+    _call("dd_beam_reorder", gpu, stream, _arg(parent, "parent", torch.int32, (B, K), gpu), B, K, c, len(states))
 
 
 def dd_paged_fork(cache: PagedCache, parent, lengths, fresh, table_out, lengths_out, stream=None):
@@ -627,23 +645,19 @@ def dd_paged_fork(cache: PagedCache, parent, lengths, fresh, table_out, lengths_
     [B*K] int32; table_out [B*K, max_pages] int32. Full pages are shared; page fresh[n], with
     the filled rows of a partly filled last page, is where beam n goes on. Outputs are other
     tensors than inputs."""
-    dev = _dev(parent, "parent")
+    gpu = _gpu(parent, "parent")
     if parent.dim() != 2:
         raise ValueError("parent must be [B, K]")
     B, K = parent.shape
     n = B * K
-    cache._sequences(n)
-    if cache.device != dev:
-        raise ValueError(f"parent is on {dev}, the cache on {cache.device}")
+    cache._fits(n, gpu)
     i32 = torch.int32
-    pp = _arg(parent, "parent", i32, (B, K), dev)
-    lp, fp, lo = (_arg(t, name, i32, (n,), dev) for t, name in
-                  ((lengths, "lengths"), (fresh, "fresh"), (lengths_out, "lengths_out")))
-    to = _arg(table_out, "table_out", i32, (n, cache.max_pages), dev, packed=False)
-    with _On(dev):
-        st = lib().dd_paged_fork(cache._ref(), pp, B, K, lp, fp, to,
-                                 table_out.stride(0) if n > 1 else cache.max_pages, lo, _stream(stream))
-    _check("dd_paged_fork", st)
+    pp = _arg(parent, "parent", i32, (B, K), gpu)
+    lp = _arg(lengths, "lengths", i32, (n,), gpu)
+    fp = _arg(fresh, "fresh", i32, (n,), gpu)
+    lo = _arg(lengths_out, "lengths_out", i32, (n,), gpu)
+    to, ts = _rows(table_out, "table_out", i32, (n, cache.max_pages), gpu)
+    _call("dd_paged_fork", gpu, stream, cache._ref, pp, B, K, lp, fp, to, ts if n > 1 else cache.max_pages, lo)
 
 
 def dd_get_device_error(stream=None) -> int:
