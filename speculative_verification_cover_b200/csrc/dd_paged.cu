@@ -36,6 +36,7 @@ struct PagedArgs {
   const int32_t* lengths;
   int B, Hq, G, heads, blocks;  // query heads per kv head; per block; blocks per kv head
   int max_len;
+  bool even_pages;             // a page holds whole groups of 16 slots
   float scale2;                // softmax scale * log2(e)
   char* out;
   float* lse;
@@ -47,7 +48,8 @@ struct PagedArgs {
   float2* part_ml;             // [2 grid][heads] (m, l) of the partial results, log2 units
   float* part_o;               // [2 grid][heads][d]
   float* lse2;                 // [B, Hq] in log2 units, of unsplit sequence-heads
-  float* scores;               // [B, Hq, max_len], log2 units (masses only)
+  float* scores;               // [B, Hq, row], log2 units (masses only)
+  int64_t score_row;           // max_len rounded up to 4
   int grid;
 };
 
@@ -164,6 +166,7 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ float s_m[kPagedWarps][GB], s_l[kPagedWarps][GB];
   __shared__ float s_o[kPagedWarps][GB][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
   const int share = plan_tiles(a, prefix, warp_tmp);
   write_empty_rows<T>(a, prefix, D);
   const int total = prefix[a.B];
@@ -253,7 +256,7 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
       const int c = lane >> SH, iu = c / GB, ig = c % GB;
       const float sc = (held >> iu) & 1u ? s[0] : -INFINITY;
       if (a.scores && (lane & ((1 << SH) - 1)) == 0 && ig < nh && j + iu < j1)
-        a.scores[((int64_t)b * a.Hq + h0 + ig) * a.max_len + j + iu] = sc;
+        a.scores[((int64_t)b * a.Hq + h0 + ig) * a.score_row + j + iu] = sc;
       float mx = sc;
 #pragma unroll
       for (int bit = 16; bit >= 32 / U; bit >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, bit));
@@ -387,21 +390,25 @@ struct Cursor {
 
 constexpr int kWarpSlots = 16;  // slots of a tile per warp
 
-template <int D, int NT>
+// Stages of a warp's ring. Two CTAs an SM with three stages keep the most bytes in flight,
+// which one long sequence wants (131071 slots, 8 kv heads: 88.7 us, against 92.9 with three
+// CTAs of two stages). Where there are as many sequence-heads as SMs their ends and starts
+// cost more, and a third CTA works through them (7 sequences of 32 kv heads: 26.9 us against
+// 29.0; 64 of 4: 109.5 against 111.0).
+template <int D, int NT, int S>
 struct MmaCfg {
-  static constexpr int kStages = D == 128 && NT == 2 ? 2 : 3;  // two CTAs per SM
+  static constexpr int kStages = S;
+  static constexpr int kCtas = S == 2 && NT == 1 ? 3 : 2;  // per SM
   static constexpr int kRowBytes = D * 2;
   static constexpr int kHalf = kWarpSlots * kRowBytes;  // K, or V, of one stage
   static constexpr int kSmem = kPagedWarps * kStages * 2 * kHalf;
-  // a warp's results at the end of a sequence-head, [heads][d] fp32, go where its last
-  // stage was
-  static_assert(NT * 8 * D * 4 <= 2 * kHalf);
+  static_assert(8 * D * 4 <= kHalf);  // results at the end of a sequence-head
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kPagedThreads, 2)
+template <int D, int NT, int S>
+__global__ void __launch_bounds__(kPagedThreads, MmaCfg<D, NT, S>::kCtas)
 paged_mma_kernel(const __grid_constant__ PagedArgs a) {
-  using C = MmaCfg<D, NT>;
+  using C = MmaCfg<D, NT, S>;
   constexpr int H = NT * 8;       // heads, padded
   constexpr int KS = D / 16;      // k-steps of S, row tiles of O
   constexpr int CH = D / 8;       // 16-byte chunks of a row
@@ -409,8 +416,10 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int warp_tmp[kPagedWarps];
   __shared__ float s_m[kPagedWarps][H], s_l[kPagedWarps][H];
+  __shared__ int64_t s_new[kPagedWarps][C::kStages];  // where a stage's new token goes
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
   const int share = plan_tiles(a, prefix, warp_tmp);
   write_empty_rows<__nv_bfloat16>(a, prefix, D);
   const int u0 = blockIdx.x * share, u_end = min(prefix[a.B], u0 + share);
@@ -426,12 +435,19 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
     id = j < lc.len ? a.c.table[(int64_t)lc.b * a.c.table_stride + div_fast(a.c.page, j)] : -1;
   };
+  // the queries of a sequence-head are read when its tiles come up: into L2 before that
+  const auto prefetch_q = [&](const Cursor& x) {
+    const int kvh = x.pair / a.blocks, blk = x.pair - kvh * a.blocks;
+    const int lines = min(a.heads, a.G - blk * a.heads) * (C::kRowBytes / 128);
+    if (lane < lines)
+      prefetch_l2(a.q + (int64_t)x.b * a.q_bytes + (int64_t)(kvh * a.G + blk * a.heads) * C::kRowBytes + lane * 128);
+  };
   fetch_id();
   uint64_t held_q = 0;  // 16 bits per stage: slots that count
   const auto issue = [&](int stage) {
     if (lu < u_end) {
       const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
-      const int kvh = lc.pair / a.blocks, blk = lc.pair - kvh * a.blocks;
+      const int kvh = lc.pair / a.blocks;
       const int page = checked_page(id, a.c.n_pages);
       const bool ok = page >= 0;  // j < len is in the id
       int64_t off = 0;
@@ -441,36 +457,43 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
       const uint32_t held = __ballot_sync(0xffffffffu, ok) & 0xffffu;
       const uint32_t fresh = __ballot_sync(0xffffffffu, ok && a.k_new && j == lc.len - 1) & 0xffffu;
       held_q = (held_q & ~(0xffffull << (16 * stage))) | ((uint64_t)held << (16 * stage));
+      if ((fresh >> (lane & 15)) & 1u) s_new[warp][stage] = off;  // both lanes of the slot: the same
       const uint32_t dst = ring + stage * 2 * C::kHalf;
-      const int c = lane % CH;
+      const int c = lane % CH, r0 = lane / CH;
+      if (a.even_pages && !fresh) {  // 16 rows of one page: one address and a stride
+        const int64_t o = __shfl_sync(0xffffffffu, off, 0) + r0 * a.c.token_bytes + c * 16;
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const char* base = kv ? a.c.v : a.c.k;
+        for (int kv = 0; kv < 2; ++kv) {
+          const char* src = (kv ? a.c.v : a.c.k) + o;
 #pragma unroll
-        for (int i = 0; i < kWarpSlots / RPI; ++i) {
-          const int r = i * RPI + lane / CH;
-          const int64_t o = __shfl_sync(0xffffffffu, off, r);
-          const uint32_t to = dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4);
-          if (!((fresh >> r) & 1u)) cp_async16(to, base + o + c * 16, (held >> r) & 1u ? 16 : 0);
+          for (int i = 0; i < kWarpSlots / RPI; ++i) {
+            const int r = i * RPI + r0;
+            cp_async16(dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4), src, (held >> r) & 1u ? 16 : 0);
+            src += RPI * a.c.token_bytes;
+          }
+          if (kv == 0) cp_async_commit();
         }
-        if (kv == 0) cp_async_commit();
-      }
-      if (fresh) {  // the new token: read from the caller, kept in the cache
-        const int r = __ffs(fresh) - 1;
-        const int64_t o = __shfl_sync(0xffffffffu, off, r);
-        for (int x = lane; x < 2 * CH; x += 32) {
-          const int kv = x / CH, cc = x - kv * CH;
-          const char* src = (kv ? a.v_new : a.k_new) + (int64_t)lc.b * a.new_bytes + kvh * C::kRowBytes + cc * 16;
-          const uint4 w = *reinterpret_cast<const uint4*>(src);
-          const uint32_t to = dst + kv * C::kHalf + r * C::kRowBytes + ((cc ^ (r & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
-          if (blk == 0) *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + o + cc * 16) = w;
+      } else {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const char* base = kv ? a.c.v : a.c.k;
+#pragma unroll
+          for (int i = 0; i < kWarpSlots / RPI; ++i) {
+            const int r = i * RPI + r0;
+            const char* src = base + __shfl_sync(0xffffffffu, off, r);
+            if ((fresh >> r) & 1u)  // the new token: read from the caller
+              src = (kv ? a.v_new : a.k_new) + (int64_t)lc.b * a.new_bytes + kvh * C::kRowBytes;
+            cp_async16(dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4), src + c * 16,
+                       (held >> r) & 1u ? 16 : 0);
+          }
+          if (kv == 0) cp_async_commit();
         }
       }
       cp_async_commit();
       if (++lu < u_end) {
         lc.next(a, prefix, lu);
         fetch_id();
+        if (lc.tile == 0 && warp == 0) prefetch_q(lc);
       }
     } else {  // empty groups keep the count
       cp_async_commit();
@@ -490,6 +513,15 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     const int kvh = cc.pair / a.blocks, blk = cc.pair - kvh * a.blocks;
     const int h0 = kvh * a.G + blk * a.heads;
     const int nh = min(a.heads, a.G - blk * a.heads);
+    // the tile of this piece, if any, whose slots of this warp hold the new token
+    const int new_tile = a.k_new && blk == 0 && ((len - 1) % kTile) / kWarpSlots == warp ? tiles - 1 - tile0 : -1;
+    const int new_row = (len - 1) & (kWarpSlots - 1);
+    const auto row_chunk = [&](uint32_t base, int r) {  // this lane's 16 bytes of a staged row
+      uint4 w;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "r"(base + r * C::kRowBytes + (((lane % CH) ^ (r & 7)) << 4)) : "memory");
+      return w;
+    };
     uint32_t q[NT][KS][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -541,11 +573,11 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         if (a.scores) {
           const int j = (tile0 + i) * kTile + warp * kWarpSlots + (lane >> 2);
           const int g = t * 8 + 2 * (lane & 3);
-          float* sp = a.scores + ((int64_t)b * a.Hq + h0 + g) * a.max_len + j;
+          float* sp = a.scores + ((int64_t)b * a.Hq + h0 + g) * a.score_row + j;
           if (g < nh && j < len) sp[0] = s[t][0];
           if (g < nh && j + 8 < len) sp[8] = s[t][2];
-          if (g + 1 < nh && j < len) sp[a.max_len] = s[t][1];
-          if (g + 1 < nh && j + 8 < len) sp[a.max_len + 8] = s[t][3];
+          if (g + 1 < nh && j < len) sp[a.score_row] = s[t][1];
+          if (g + 1 < nh && j + 8 < len) sp[a.score_row + 8] = s[t][3];
         }
         float mx[2] = {fmaxf(s[t][0], s[t][2]), fmaxf(s[t][1], s[t][3])};
         float p[4];
@@ -588,6 +620,13 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
           mma16816(o[k][t], f, pl[t][0], pl[t][1]);
         }
       }
+      if (i == new_tile && ((held >> new_row) & 1u)) {  // the new token, from its row here, into the cache
+        const int64_t to = s_new[warp][stage] + (lane % CH) * 16;
+        if (lane < CH) {
+          *reinterpret_cast<uint4*>(a.c.k + to) = row_chunk(kb, new_row);
+          *reinterpret_cast<uint4*>(a.c.v + to) = row_chunk(vb, new_row);
+        }
+      }
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
     // ---- join the four warps
@@ -601,22 +640,25 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         l[t][e] = x;
       }
-    // the stage read last is free until the next copy into it, which comes after the join;
-    // element e of a head's row lies at e ^ (8 * (head / 2 % 4)), which spreads the heads a
-    // warp writes at once over the banks
+    // the stage read last is not refilled before the join: its place takes a warp's results,
+    // [8 heads][d] fp32 at a time; element e of a head's row lies at
+    // e ^ (8 * (head / 2 % 4)), which spreads the heads a warp writes at once over the banks
     const int last = stage == 0 ? C::kStages - 1 : stage - 1;
     const auto joined = [&](int w) {
       return reinterpret_cast<float*>(smem + (w * C::kStages + last) * 2 * C::kHalf);
     };
     __syncwarp();
+    const bool starts = tile0 == 0, whole = starts && n_tiles == tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+      if (t > 0) __syncthreads();  // the first eight heads' results are read
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int g = t * 8 + 2 * (lane & 3) + e;
+        const int g = 2 * (lane & 3) + e;
         if (lane < 4) {
-          s_m[warp][g] = m[t][e];
-          s_l[warp][g] = l[t][e];
+          s_m[warp][t * 8 + g] = m[t][e];
+          s_l[warp][t * 8 + g] = l[t][e];
         }
         float* op = joined(warp) + g * D;
         const int x = (lane & 3) << 3;
@@ -626,38 +668,37 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
           op[(k * 16 + 8 + (lane >> 2)) ^ x] = o[k][t][e + 2];
         }
       }
-    __syncthreads();
-    const bool starts = tile0 == 0, whole = starts && n_tiles == tiles;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-    for (int i = threadIdx.x; i < nh * (D / 4); i += kPagedThreads) {
-      const int g = i / (D / 4), e = (i - g * (D / 4)) * 4;
-      float mm = s_m[0][g];
+      __syncthreads();
+      for (int i = threadIdx.x; i < min(nh - t * 8, 8) * (D / 4); i += kPagedThreads) {
+        const int gt = i / (D / 4), e = (i - gt * (D / 4)) * 4, g = t * 8 + gt;
+        float mm = s_m[0][g];
 #pragma unroll
-      for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) {
-        const float f = exp2f(s_m[w][g] - base);
-        ll = fmaf(s_l[w][g], f, ll);
-        const float4 x = *reinterpret_cast<const float4*>(joined(w) + g * D + (e ^ (((g >> 1) & 3) << 3)));
-        oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
-        oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
-      }
-      if (whole) {
-        const int64_t h = (int64_t)b * a.Hq + h0 + g;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
-        const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
-        *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
-        if (e == 0) {
-          const float z2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
-          a.lse2[h] = z2;
-          if (a.lse) a.lse[h] = z2 * kLn2;
+        for (int w = 0; w < kPagedWarps; ++w) {
+          const float f = exp2f(s_m[w][g] - base);
+          ll = fmaf(s_l[w][g], f, ll);
+          const float4 x = *reinterpret_cast<const float4*>(joined(w) + gt * D + (e ^ (((gt >> 1) & 3) << 3)));
+          oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
+          oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
         }
-      } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
-        *reinterpret_cast<float4*>(a.part_o + (slot * a.heads + g) * D + e) = oo;
-        if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
+        if (whole) {
+          const int64_t h = (int64_t)b * a.Hq + h0 + g;
+          const float inv = ll > 0.f ? 1.f / ll : 0.f;
+          const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
+          *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
+          if (e == 0) {
+            const float z2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
+            a.lse2[h] = z2;
+            if (a.lse) a.lse[h] = z2 * kLn2;
+          }
+        } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
+          *reinterpret_cast<float4*>(a.part_o + (slot * a.heads + g) * D + e) = oo;
+          if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
+        }
       }
     }
     u += n_tiles;
@@ -691,7 +732,7 @@ __device__ __forceinline__ int64_t part_slot(const Span& s, int c) {
 
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kMassChunk = 256;  // slots per step of a mass CTA
+constexpr int kMassChunk = 128;  // slots per step of a mass CTA: four to a lane, warps share the heads
 
 // (m, l) of the union of two parts.
 __device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2) {
@@ -703,14 +744,16 @@ __device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2)
 
 // CTAs [0, B Hq): the output of one (sequence, query head) that was split, its parts over
 // four warps. The rest, mass_ctas to a sequence: the masses, from the scores the main
-// kernel left and the joined log-sums, which each CTA forms for its sequence (4 lanes to a
-// head) rather than waiting for another kernel's.
+// kernel left and the joined log-sums. Each warp takes eight heads at a time, forms their
+// log-sums (4 lanes to a head) rather than waiting for another kernel's, and adds up their
+// part of the CTA's slots.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
   pdl_wait();
   constexpr int N = D / 32;
-  extern __shared__ float z2[];  // [Hq rounded up to 8] of this sequence, log2 units (mass CTAs)
+  extern __shared__ float z2[];  // [Hq rounded up to 8] of this sequence, log2 units (mass CTAs);
+                                // a warp's heads are written and read by that warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t heads = (int64_t)a.B * a.Hq;
   if (blockIdx.x < heads) {
@@ -778,9 +821,20 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
   const int k = (int)(blockIdx.x - heads), b = k / mass_ctas, part = k - b * mass_ctas;
   const int len = checked_length(a.lengths, b, a.max_len);
   if (part * kMassChunk >= len) return;
-  const int padded = (a.Hq + 7) & ~7;
-  for (int h0 = 0; h0 < padded; h0 += kJoinThreads / 4) {  // 4 lanes to a head
-    const int h = h0 + (threadIdx.x >> 2);
+  __shared__ float4 s_sum[kJoinWarps][32];
+  const float* scores = a.scores + (int64_t)b * a.Hq * a.score_row;
+  int j = part * kMassChunk + 4 * lane;
+  // the scores of eight heads; the first eight are under way while the log-sums are formed
+  float4 x[8];
+  const auto load = [&](int h) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (j < len)
+        x[e] = *reinterpret_cast<const float4*>(scores + min(h + e, a.Hq - 1) * a.score_row + j);
+  };
+  load(8 * warp);
+  for (int h0 = 8 * warp; h0 < a.Hq; h0 += 8 * kJoinWarps) {
+    const int h = h0 + (lane >> 2);
     float m = -INFINITY, l = 0.f;
     bool whole = false;
     if (h < a.Hq) {
@@ -802,32 +856,39 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
       if (!whole) merge_ml(m, l, m2, l2);
     }
-    // a head without weights adds none: e^{s - inf} = 0
-    if ((lane & 3) == 0 && h < padded)
+    // a head without weights (or behind the last) adds none: e^{s - inf} = 0
+    if ((lane & 3) == 0)
       z2[h] = h >= a.Hq || m == -INFINITY ? INFINITY : whole ? m : m + log2f(l);
   }
-  __syncthreads();
+  __syncwarp();
   const float inv = 1.f / (float)a.Hq;
-  const float* scores = a.scores + (int64_t)b * a.Hq * a.max_len;
-  for (int j = part * kMassChunk + threadIdx.x; j < len; j += kMassChunk * mass_ctas) {
+  for (int first = part * kMassChunk; first < len; first += kMassChunk * mass_ctas) {
+    j = first + 4 * lane;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int h = 8 * warp; h < a.Hq; h += 8 * kJoinWarps) {
+      if (h > 8 * warp || first > part * kMassChunk) load(h);
 #pragma unroll
-    for (int half = 0; half < kMassChunk / kJoinThreads; ++half) {
-      const int jj = j + half * kJoinThreads;
-      if (jj >= len) break;
-      float sum = 0.f;
-      for (int h = 0; h < a.Hq; h += 8) {
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[e] = scores[(int64_t)min(h + e, a.Hq - 1) * a.max_len + jj];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += exp2f(x[e] - z2[h + e]);
+      for (int e = 0; e < 8; ++e) {
+        const float z = z2[h + e];
+        sum.x += exp2f(x[e].x - z);
+        sum.y += exp2f(x[e].y - z);
+        sum.z += exp2f(x[e].z - z);
+        sum.w += exp2f(x[e].w - z);
       }
-      const int64_t at = (int64_t)b * a.mass_stride + jj;
-      const bool fresh = a.k_new && jj == len - 1;
-      const float before = a.mass_in && !fresh ? a.mass_in[at] : 0.f;
-      a.mass_out[at] = before + sum * inv;
     }
+    s_sum[warp][lane] = sum;
+    __syncthreads();
+    const int at = first + threadIdx.x;  // a slot a thread
+    if (at < len) {
+      float total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) total += reinterpret_cast<const float*>(s_sum[w])[threadIdx.x];
+      const int64_t o = (int64_t)b * a.mass_stride + at;
+      const bool fresh = a.k_new && at == len - 1;
+      const float before = a.mass_in && !fresh ? a.mass_in[o] : 0.f;
+      a.mass_out[o] = before + total * inv;
+    }
+    __syncthreads();
   }
 }
 
@@ -837,6 +898,7 @@ struct PagedWorkspace {
 // Heads of one block: a kv head's query heads in as few equal blocks as the limit allows.
 int head_blocks(int G, int limit) { return (G + limit - 1) / limit; }
 
+int64_t score_row(int max_len) { return ((int64_t)max_len + 3) & ~3ll; }
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 PagedWorkspace paged_layout(int B, int Hq, int d, int max_len, bool mass, int heads) {
@@ -851,20 +913,26 @@ PagedWorkspace paged_layout(int B, int Hq, int d, int max_len, bool mass, int he
   w.ml = take((size_t)2 * kMaxPagedGrid * heads * 8);
   w.o = take((size_t)2 * kMaxPagedGrid * heads * d * 4);
   w.lse2 = take((size_t)B * Hq * 4);
-  w.scores = take(mass ? (size_t)B * Hq * max_len * 4 : 0);
+  w.scores = take(mass ? (size_t)B * Hq * score_row(max_len) * 4 : 0);
   w.total = at;
   return w;
 }
 
+int paged_grid(int64_t tiles, int per_sm) {
+  int64_t most = (int64_t)device_info().sm_count * per_sm;
+  if (most > kMaxPagedGrid) most = kMaxPagedGrid;
+  return (int)(tiles < most ? tiles : most);
+}
+
 template <typename T, int D>
-cudaError_t launch_simt(const PagedArgs& a, size_t smem, cudaStream_t stream) {
+cudaError_t launch_simt(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
+  a.grid = paged_grid(tiles, 4);
   switch (a.heads) {
-    case 1: paged_simt_kernel<T, D, 1><<<a.grid, kPagedThreads, smem, stream>>>(a); break;
-    case 2: paged_simt_kernel<T, D, 2><<<a.grid, kPagedThreads, smem, stream>>>(a); break;
-    case 3: case 4: paged_simt_kernel<T, D, 4><<<a.grid, kPagedThreads, smem, stream>>>(a); break;
-    default: paged_simt_kernel<T, D, 8><<<a.grid, kPagedThreads, smem, stream>>>(a); break;
+    case 1: return launch_dependent(paged_simt_kernel<T, D, 1>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
+    case 2: return launch_dependent(paged_simt_kernel<T, D, 2>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
+    case 3: case 4: return launch_dependent(paged_simt_kernel<T, D, 4>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
+    default: return launch_dependent(paged_simt_kernel<T, D, 8>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
   }
-  return cudaGetLastError();
 }
 
 // bf16: up to 16 heads in one pass over the cache (two column tiles); fp32: 8.
@@ -873,18 +941,26 @@ int heads_per_block(int G, bool bf16) {
   return (G + blocks - 1) / blocks;
 }
 
-template <int D, int NT>
-cudaError_t launch_mma(const PagedArgs& a, size_t smem, cudaStream_t stream) {
+template <int D, int NT, int S>
+cudaError_t launch_mma(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
+  using C = MmaCfg<D, NT, S>;
   static thread_local int configured_for = -1;
-  const int bytes = MmaCfg<D, NT>::kSmem + (int)smem;
-  if (configured_for != device_info().device) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               MmaCfg<D, NT>::kSmem + (kPagedMaxBatch + 1) * 4);
+  const DeviceInfo& dev = device_info();
+  if (configured_for != dev.device) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               C::kSmem + (kPagedMaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
-    configured_for = device_info().device;
+    configured_for = dev.device;
   }
-  paged_mma_kernel<D, NT><<<a.grid, kPagedThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  a.grid = paged_grid(tiles, C::kCtas);
+  return launch_dependent(paged_mma_kernel<D, NT, S>, dim3(a.grid), dim3(kPagedThreads), C::kSmem + smem, stream, a);
+}
+
+template <int D>
+cudaError_t launch_bf16(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
+  if (a.heads > 8) return launch_mma<D, 2, D == 128 ? 2 : 3>(a, tiles, smem, stream);
+  if ((int64_t)a.B * a.c.Hkv * a.blocks >= device_info().sm_count) return launch_mma<D, 1, 2>(a, tiles, smem, stream);
+  return launch_mma<D, 1, 3>(a, tiles, smem, stream);
 }
 
 }  // namespace
@@ -936,6 +1012,7 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.heads = heads_per_block(a.G, c.dtype == DD_BF16);
   a.blocks = (a.G + a.heads - 1) / a.heads;
   a.max_len = p.max_len;
+  a.even_pages = c.page_size % kWarpSlots == 0;
   a.scale2 = (p.scale > 0.f ? p.scale : 1.f / sqrtf((float)c.d)) * kLog2e;
   a.out = static_cast<char*>(p.out);
   a.lse = p.lse;
@@ -946,18 +1023,15 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
+  a.score_row = score_row(p.max_len);
   a.scores = p.mass_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   const int64_t tiles = (int64_t)p.B * c.Hkv * a.blocks * ((p.max_len + kTile - 1) / kTile);
-  const int64_t most = min((int64_t)kMaxPagedGrid,
-                           (int64_t)device_info().sm_count * (c.dtype == DD_BF16 ? 2 : 4));
-  a.grid = (int)(tiles < most ? tiles : most);
   const size_t smem = ((size_t)p.B + 1) * 4;
   cudaError_t err;
   if (c.dtype == DD_BF16)
-    err = a.heads > 8 ? (c.d == 128 ? launch_mma<128, 2>(a, smem, stream) : launch_mma<64, 2>(a, smem, stream))
-                      : (c.d == 128 ? launch_mma<128, 1>(a, smem, stream) : launch_mma<64, 1>(a, smem, stream));
+    err = c.d == 128 ? launch_bf16<128>(a, tiles, smem, stream) : launch_bf16<64>(a, tiles, smem, stream);
   else
-    err = c.d == 128 ? launch_simt<float, 128>(a, smem, stream) : launch_simt<float, 64>(a, smem, stream);
+    err = c.d == 128 ? launch_simt<float, 128>(a, tiles, smem, stream) : launch_simt<float, 64>(a, tiles, smem, stream);
   if (err != cudaSuccess) return err;
   // join: a CTA per query head; masses: enough CTAs a sequence to fill the GPU a few times
   int mass_ctas = 0;
