@@ -69,21 +69,14 @@ __device__ __forceinline__ bool scans(const float* score_in, const uint8_t* done
   return s > -INFINITY && !d;
 }
 
-// The largest 16-bit p that at least `want` of the 256 keys reach (0 if fewer are above 0),
-// bit by bit, by one warp.
-__device__ __forceinline__ uint32_t kth_key16(const uint16_t* keys, int want) {
-  const uint4 w = *reinterpret_cast<const uint4*>(keys + (threadIdx.x & 31) * 8);
-  const uint32_t k[8] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16,
-                         w.z & 0xffffu, w.z >> 16, w.w & 0xffffu, w.w >> 16};
+// The largest 16-bit p that at least `want` of the block's keys reach, bit by bit; all threads
+// call it. (A barrier that counts costs 60 cycles a bit; one warp over all keys, 300 for two
+// bits.)
+__device__ __forceinline__ uint32_t kth_key16(uint32_t key, int want) {
   uint32_t p = 0;
-#pragma unroll
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t c = p | (1u << bit);
-    int n = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) n += k[e] >= c;
-    if (__reduce_add_sync(0xffffffffu, n) >= want) p = c;
-  }
+#pragma unroll 1  // a kernel's first pass waits for its instructions: short code
+  for (int bit = 15; bit >= 0; --bit)
+    if (__syncthreads_count(key >= (p | (1u << bit))) >= want) p |= 1u << bit;
   return p;
 }
 
@@ -104,7 +97,6 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   constexpr int kPiece = beam_piece<T>();
   extern __shared__ __align__(128) uint8_t piece_smem[];  // [kPieceBytes]
   __shared__ __align__(8) uint64_t bar;
-  __shared__ __align__(16) uint16_t s_key[kBeamThreads];
   __shared__ uint2 s_list[kBeamList];   // (key, index in the piece)
   __shared__ uint8_t s_seg[kBeamThreads];
   __shared__ float2 s_ml[kBeamWarps + kBeamWarps / 2];  // and the radix select's scan
@@ -144,12 +136,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   }
   const float mx = max_of(max_word(max_word(mw[0], mw[1], T{}), max_word(mw[2], mw[3], T{}), T{}), T{}) + 0.f;
   const uint32_t mine = logit_key(mx) >> 16;
-  s_key[threadIdx.x] = (uint16_t)mine;
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t p = kth_key16(s_key, K);
-    if (lane == 0) s_bound = p;
-  }
+  const uint32_t bound = kth_key16(mine, K);
   // sum of exponentials relative to the segment's maximum
   const float ref2 = mx * kLog2e;  // rounded once: the sum is relative to exactly 2^ref2
   const float ref = mx > -INFINITY ? ref2 : 0.f;
@@ -188,7 +175,6 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_ml[warp] = make_float2(m, sum);
   __syncthreads();
-  const uint32_t bound = s_bound;
   if (mine >= bound && mx > -INFINITY) s_seg[atomicAdd(&s_segs, 1)] = (uint8_t)threadIdx.x;
   __syncthreads();
   const int segs = s_segs;
@@ -302,10 +288,10 @@ __device__ __forceinline__ bool better(double s, int64_t at, double s2, int64_t 
   return s > s2 || (s == s2 && at < at2);
 }
 
-// What the merge holds on chip from its first loads: entries per thread, and the sums of
-// rows of up to so many pieces (more are read again where they are needed).
-constexpr int kHeldEntries = 12;
-constexpr int kHeldPieces = 24;
+// What the merge holds in shared memory from its first loads: entries, and lists' sums (more
+// are read again where they are needed).
+constexpr int kHeldEntries = 3072;
+constexpr int kHeldLists = 512;
 
 struct BeamOut {
   int32_t* parent;
@@ -337,24 +323,22 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
   extern __shared__ uint8_t head[];  // [K * pieces]
   __shared__ double s_base[kBeamMaxK];
   __shared__ uint8_t s_kind[kBeamMaxK];  // 0 no candidate, 1 live, 2 done
+  __shared__ float s_max[kBeamMaxK];
+  __shared__ double s_sum[kBeamMaxK];
   __shared__ Best s_best[kBeamWarps];
-  __shared__ float2 s_ml[kBeamMaxK * kHeldPieces];
+  __shared__ float2 s_ml[kHeldLists];
+  __shared__ uint2 s_cand[kHeldEntries];
   __shared__ double s_score[kBeamList];
   __shared__ int64_t s_at[kBeamList];
-  __shared__ __align__(16) uint16_t s_key[kBeamThreads];
-  __shared__ uint32_t s_bound;
   __shared__ int s_n;
   const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lists = K * pieces, entries = lists * K;
-  const uint2* mine = cand + (int64_t)b * entries;
+  const int lists = K * pieces;
+  const uint2* mine = cand + (int64_t)b * lists * K;
   // everything is loaded at once: the lists' entries do not wait for the sums
-  uint2 held[kHeldEntries];
-#pragma unroll
-  for (int e = 0; e < kHeldEntries; ++e) {
-    const int i = e * kBeamThreads + threadIdx.x;
-    held[e] = i < entries ? mine[i] : make_uint2(kNone, 0u);
-  }
-  const bool small = pieces <= kHeldPieces;
+  const int per_beam = pieces * K, entries = K * per_beam;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < min(entries, kHeldEntries); i += kBeamThreads) s_cand[i] = mine[i];
+  const bool small = lists <= kHeldLists;
   if (small)
     for (int i = threadIdx.x; i < lists; i += kBeamThreads) s_ml[i] = ml[(int64_t)b * lists + i];
   if (threadIdx.x < K) {
@@ -377,40 +361,43 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
       for (int i = lane; i < pieces; i += 32) z += (double)p[i].y * (double)exp2f(p[i].x - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    __syncwarp();
     if (lane == 0) {
-      if (m > -INFINITY) s_base[k] -= (double)m / (double)kLog2e + log(z);
-      else s_kind[k] = 0;
+      s_max[k] = m;
+      s_sum[k] = z;
     }
   }
   __syncthreads();
-  // candidate i: entry i of the lists, or the one of done beam i - entries
-  const auto score_of = [&](int i, const uint2& c, double& s, int64_t& at) {
-    const int k = i / (pieces * K);
+  if (threadIdx.x < K && s_kind[threadIdx.x] == 1) {
+    const float m = s_max[threadIdx.x];
+    if (m > -INFINITY) s_base[threadIdx.x] -= (double)m * (1.0 / (double)kLog2e) + log(s_sum[threadIdx.x]);
+    else s_kind[threadIdx.x] = 0;
+  }
+  __syncthreads();
+  // an entry of live beam k; the one candidate of done beam k
+  const auto entry = [&](int k, const uint2& c, double& s, int64_t& at) {
     if (s_kind[k] != 1 || c.x <= kNone) return false;
     s = s_base[k] + (double)key_logit(c.x);
     at = (int64_t)k * V + c.y;
     return true;
   };
-  const auto get = [&](int i, double& s, int64_t& at) {
-    if (i < entries) return score_of(i, mine[i], s, at);
-    const int k = i - entries;
+  const auto ended = [&](int k, double& s, int64_t& at) {
     if (s_kind[k] != 2) return false;
     s = s_base[k];
     at = (int64_t)k * V + (res.eos > 0 ? res.eos : 0);
     return true;
   };
-  const auto each = [&](auto f) {  // of this thread's candidates
+  // this thread's candidates: warp w has beams w, w + 8, ..., a lane every 32nd entry
+  const auto each = [&](auto f) {
     double s;
     int64_t at;
-#pragma unroll
-    for (int e = 0; e < kHeldEntries; ++e) {
-      const int i = e * kBeamThreads + threadIdx.x;
-      if (held[e].x > kNone && score_of(i, held[e], s, at)) f(s, at);
+#pragma unroll 1
+    for (int k = warp; k < K; k += kBeamWarps) {
+      if (s_kind[k] == 1)
+#pragma unroll 2
+        for (int i = k * per_beam + lane; i < (k + 1) * per_beam; i += 32)
+          if (entry(k, i < kHeldEntries ? s_cand[i] : mine[i], s, at)) f(s, at);
+      if (lane == 0 && ended(k, s, at)) f(s, at);
     }
-    for (int i = kHeldEntries * kBeamThreads + threadIdx.x; i < entries; i += kBeamThreads)
-      if (get(i, s, at)) f(s, at);
-    if (threadIdx.x < K && get(entries + threadIdx.x, s, at)) f(s, at);
   };
   double top = -INFINITY;
   each([&](double s, int64_t) { top = fmax(top, s); });
@@ -424,15 +411,8 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
   const auto near = [&](double s) {  // 16 bits, larger nearer to the best; 0: none
     return s > -INFINITY ? 0xFFFFu - (__float_as_uint((float)(best - s)) >> 16) : 0u;
   };
-  s_key[threadIdx.x] = (uint16_t)near(top);
-  __syncthreads();
-  if (warp == 0) {
-    const uint32_t p = kth_key16(s_key, K);
-    if (lane == 0) s_bound = p;
-  }
-  __syncthreads();
-  const uint32_t bound = s_bound;
-  if (s_key[threadIdx.x] >= bound)
+  const uint32_t bound = kth_key16(near(top), K);
+  if (near(top) >= bound)
     each([&](double s, int64_t at) {
       if (near(s) < bound) return;
       const int n = atomicAdd(&s_n, 1);
@@ -465,8 +445,7 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
       const int k = i / pieces, h = head[i];
       double s;
       int64_t at;
-      if (s_kind[k] == 1 ? h < K && get(i * K + h, s, at)
-                         : h == 0 && i == k * pieces && get(entries + k, s, at))
+      if (s_kind[k] == 1 ? h < K && entry(k, mine[i * K + h], s, at) : h == 0 && i == k * pieces && ended(k, s, at))
         if (better(s, at, o.score, o.at)) o = Best{s, at, i};
     }
   };
