@@ -14,6 +14,8 @@
 // depends on max_len.
 //
 // Bound: HBM, 2 Hkv d elements per slot read once.
+#include <cooperative_groups.h>
+
 #include "dd_paged.cuh"
 #include "dd_tc.cuh"
 
@@ -26,6 +28,12 @@ constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kMaxPagedGrid = 1024;  // bounds the workspace on any device
 constexpr int kMaxHeads = 16;    // query heads of one block at most
+constexpr int kWholeLen = 512;   // sequences up to here are not split (without masses)
+constexpr int kPairCtas = 8;     // CTAs of a sequence-head's cluster (few short sequences)
+
+// How the tiles are given to CTAs: equal ranges, joined by a second kernel; whole
+// sequence-heads; or a cluster of CTAs for each.
+enum class PagedSplit { kRanges, kWhole, kCluster };
 
 struct PagedArgs {
   PagedView c;
@@ -51,11 +59,16 @@ struct PagedArgs {
   float* scores;               // [B, Hq, row], log2 units (masses only)
   int64_t score_row;           // max_len rounded up to 4
   int grid;
+  PagedSplit split;
 };
 
+// The tiles of a CTA: [u0, u1).
+struct Share {
+  int u0, u1;
+};
 // First tile of every sequence into smem prefix[0 .. B] (and CTA 0: the workspace, for
-// the join), the tiles per CTA as the result.
-__device__ int plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) {
+// the join), and this CTA's share of the tiles.
+__device__ Share plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) {
   const int per_tile = a.c.Hkv * a.blocks;
   const int chunk = (a.B + kPagedThreads - 1) / kPagedThreads;
   const int b0 = min(a.B, (int)threadIdx.x * chunk), b1 = min(a.B, b0 + chunk);
@@ -79,9 +92,21 @@ __device__ int plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) {
   for (int b = b0; b < b1; ++b) prefix[b] += before;
   if (threadIdx.x == kPagedThreads - 1) prefix[a.B] = before + sum;
   __syncthreads();
+  if (a.split == PagedSplit::kCluster) return Share{0, 0};  // the caller's
+  if (a.split == PagedSplit::kWhole) {  // as many sequence-heads a CTA as any other, give or take one
+    const int per = a.c.Hkv * a.blocks;
+    const auto start = [&](int64_t i) {  // first tile of the first sequence-head of CTA i
+      const int64_t p = i * ((int64_t)a.B * per) / a.grid;
+      const int b = (int)(p / per);
+      return b == a.B ? prefix[b] : prefix[b] + (prefix[b + 1] - prefix[b]) / per * (int)(p - (int64_t)b * per);
+    };
+    return Share{start(blockIdx.x), start(blockIdx.x + 1)};
+  }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.B; b += kPagedThreads) a.prefix[b] = prefix[b];
-  return (prefix[a.B] + a.grid - 1) / a.grid;
+  const int share = (prefix[a.B] + a.grid - 1) / a.grid;
+  const int u0 = min(prefix[a.B], (int)blockIdx.x * share);
+  return Share{u0, min(prefix[a.B], u0 + share)};
 }
 
 // The sequence that tile u belongs to: prefix[b] <= u < prefix[b + 1].
@@ -167,11 +192,10 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
   __shared__ float s_o[kPagedWarps][GB][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int share = plan_tiles(a, prefix, warp_tmp);
+  const Share share = plan_tiles(a, prefix, warp_tmp);
   write_empty_rows<T>(a, prefix, D);
-  const int total = prefix[a.B];
-  int u = blockIdx.x * share;
-  const int u_end = min(total, u + share);
+  int u = share.u0;
+  const int u_end = share.u1;
   while (u < u_end) {
     const int b = find_sequence(prefix, a.B, u);
     const int len = checked_length(a.lengths, b, a.max_len);
@@ -405,7 +429,10 @@ struct MmaCfg {
   static_assert(8 * D * 4 <= kHalf);  // results at the end of a sequence-head
 };
 
-template <int D, int NT, int S>
+// CL: a cluster of kPairCtas CTAs for each sequence-head, its tiles split among them, their
+// results joined through distributed shared memory: one launch, for few short sequences,
+// where the latency of the call is what counts.
+template <int D, int NT, int S, bool CL>
 __global__ void __launch_bounds__(kPagedThreads, MmaCfg<D, NT, S>::kCtas)
 paged_mma_kernel(const __grid_constant__ PagedArgs a) {
   using C = MmaCfg<D, NT, S>;
@@ -420,15 +447,31 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  const int share = plan_tiles(a, prefix, warp_tmp);
+  Share share = plan_tiles(a, prefix, warp_tmp);
   write_empty_rows<__nv_bfloat16>(a, prefix, D);
-  const int u0 = blockIdx.x * share, u_end = min(prefix[a.B], u0 + share);
-  if (u0 >= u_end) return;
+  // CL: the cluster's sequence and head, and this CTA's results, [head][d] in the V parts of
+  // the first stages of warps 0 (heads 0 - 7) and 1, which nobody reads any more by then
+  [[maybe_unused]] int cl_b = 0, cl_pair = 0;
+  __shared__ float cl_m[CL ? H : 1], cl_l[CL ? H : 1];
+  [[maybe_unused]] const auto cl_at = [](int g, int e) {
+    return (g / 8) * (C::kStages * 2 * C::kHalf) + C::kHalf + ((g % 8) * D + e) * 4;
+  };
+  if constexpr (CL) {
+    const int per = a.c.Hkv * a.blocks, p = blockIdx.x / kPairCtas, rank = blockIdx.x - p * kPairCtas;
+    cl_b = p / per;
+    cl_pair = p - cl_b * per;
+    const int tiles = (prefix[cl_b + 1] - prefix[cl_b]) / per;
+    if (tiles == 0) return;  // the whole cluster
+    const int each = (tiles + kPairCtas - 1) / kPairCtas, first = prefix[cl_b] + cl_pair * tiles;
+    share = Share{first + min(tiles, rank * each), first + min(tiles, (rank + 1) * each)};
+  }
+  const int u0 = share.u0, u_end = share.u1;
+  if (!CL && u0 >= u_end) return;
   const uint32_t ring = smem_u32(smem) + warp * (C::kStages * 2 * C::kHalf);
 
   // ---- copies: the page id of this lane's slot one tile ahead, then the rows
   Cursor lc;  // the tile whose page ids are held
-  lc.seek(a, prefix, u0);
+  if (!CL || u0 < u_end) lc.seek(a, prefix, u0);
   int lu = u0;
   int id = -1;
   const auto fetch_id = [&]() {
@@ -442,7 +485,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     if (lane < lines)
       prefetch_l2(a.q + (int64_t)x.b * a.q_bytes + (int64_t)(kvh * a.G + blk * a.heads) * C::kRowBytes + lane * 128);
   };
-  fetch_id();
+  if (!CL || u0 < u_end) fetch_id();
   uint64_t held_q = 0;  // 16 bits per stage: slots that count
   const auto issue = [&](int stage) {
     if (lu < u_end) {
@@ -505,7 +548,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
 
   // ---- the products
   Cursor cc;
-  cc.seek(a, prefix, u0);
+  if (!CL || u0 < u_end) cc.seek(a, prefix, u0);
   int stage = 0;
   for (int u = u0; u < u_end;) {
     const int b = cc.b, len = cc.len, tiles = cc.tiles, tile0 = cc.tile;
@@ -685,7 +728,10 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
           oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
           oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
         }
-        if (whole) {
+        if constexpr (CL) {  // kept for the cluster
+          *reinterpret_cast<float4*>(smem + cl_at(g, e)) = oo;
+          if (e == 0) { cl_m[g] = mm; cl_l[g] = ll; }
+        } else if (whole) {
           const int64_t h = (int64_t)b * a.Hq + h0 + g;
           const float inv = ll > 0.f ? 1.f / ll : 0.f;
           const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
@@ -702,11 +748,51 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
       }
     }
     u += n_tiles;
-    if (u < u_end) {
+    if (!CL && u < u_end) {
       __syncthreads();  // every warp has read the results: the stage is free
       cc.tile = tile0 + n_tiles - 1;
       cc.next(a, prefix, u);
     }
+  }
+  if constexpr (CL) {
+    namespace cg = cooperative_groups;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int kvh = cl_pair / a.blocks, blk = cl_pair - kvh * a.blocks;
+    const int h0 = kvh * a.G + blk * a.heads, nh = min(a.heads, a.G - blk * a.heads);
+    if (u0 == u_end && threadIdx.x < H) { cl_m[threadIdx.x] = -INFINITY; cl_l[threadIdx.x] = 0.f; }
+    cluster.sync();
+    const int rank = (int)cluster.block_rank();
+    for (int i = rank * kPagedThreads + threadIdx.x; i < nh * (D / 4); i += kPairCtas * kPagedThreads) {
+      const int g = i / (D / 4), e = (i - g * (D / 4)) * 4;
+      float mr[kPairCtas], lr[kPairCtas];
+      float4 x[kPairCtas];
+#pragma unroll
+      for (int r = 0; r < kPairCtas; ++r) {
+        mr[r] = *cluster.map_shared_rank(&cl_m[g], r);
+        lr[r] = *cluster.map_shared_rank(&cl_l[g], r);
+        x[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(smem + cl_at(g, e), r));
+      }
+      float mm = mr[0];
+#pragma unroll
+      for (int r = 1; r < kPairCtas; ++r) mm = fmaxf(mm, mr[r]);
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < kPairCtas; ++r) {
+        if (mr[r] == -INFINITY) continue;  // its shared memory holds no result
+        const float f = exp2f(mr[r] - base);
+        ll = fmaf(lr[r], f, ll);
+        oo.x = fmaf(x[r].x, f, oo.x); oo.y = fmaf(x[r].y, f, oo.y);
+        oo.z = fmaf(x[r].z, f, oo.z); oo.w = fmaf(x[r].w, f, oo.w);
+      }
+      const int64_t h = (int64_t)cl_b * a.Hq + h0 + g;
+      const float inv = ll > 0.f ? 1.f / ll : 0.f;
+      const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
+      *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
+      if (e == 0 && a.lse) a.lse[h] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+    }
+    cluster.sync();  // no CTA leaves while another reads its shared memory
   }
 }
 
@@ -918,6 +1004,7 @@ PagedWorkspace paged_layout(int B, int Hq, int d, int max_len, bool mass, int he
   return w;
 }
 
+int64_t sequence_heads(const PagedArgs& a) { return (int64_t)a.B * a.c.Hkv * a.blocks; }
 int paged_grid(int64_t tiles, int per_sm) {
   int64_t most = (int64_t)device_info().sm_count * per_sm;
   if (most > kMaxPagedGrid) most = kMaxPagedGrid;
@@ -941,25 +1028,46 @@ int heads_per_block(int G, bool bf16) {
   return (G + blocks - 1) / blocks;
 }
 
-template <int D, int NT, int S>
+template <int D, int NT, int S, bool CL = false>
 cudaError_t launch_mma(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
   using C = MmaCfg<D, NT, S>;
   static thread_local int configured_for = -1;
   const DeviceInfo& dev = device_info();
+  const auto kernel = paged_mma_kernel<D, NT, S, CL>;
   if (configured_for != dev.device) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_mma_kernel<D, NT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C::kSmem + (kPagedMaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
     configured_for = dev.device;
   }
-  a.grid = paged_grid(tiles, C::kCtas);
-  return launch_dependent(paged_mma_kernel<D, NT, S>, dim3(a.grid), dim3(kPagedThreads), C::kSmem + smem, stream, a);
+  if (!CL) {
+    a.grid = paged_grid(tiles, C::kCtas);
+    return launch_dependent(kernel, dim3(a.grid), dim3(kPagedThreads), C::kSmem + smem, stream, a);
+  }
+  a.grid = (int)sequence_heads(a) * kPairCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.grid);
+  cfg.blockDim = dim3(kPagedThreads);
+  cfg.dynamicSmemBytes = C::kSmem + smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPairCtas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <int D>
 cudaError_t launch_bf16(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
+  if (a.split == PagedSplit::kCluster)
+    return a.heads > 8 ? launch_mma<D, 2, D == 128 ? 2 : 3, true>(a, tiles, smem, stream)
+                       : launch_mma<D, 1, 3, true>(a, tiles, smem, stream);
   if (a.heads > 8) return launch_mma<D, 2, D == 128 ? 2 : 3>(a, tiles, smem, stream);
-  if ((int64_t)a.B * a.c.Hkv * a.blocks >= device_info().sm_count) return launch_mma<D, 1, 2>(a, tiles, smem, stream);
+  if (sequence_heads(a) >= device_info().sm_count) return launch_mma<D, 1, 2>(a, tiles, smem, stream);
   return launch_mma<D, 1, 3>(a, tiles, smem, stream);
 }
 
@@ -1027,12 +1135,26 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.scores = p.mass_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
   const int64_t tiles = (int64_t)p.B * c.Hkv * a.blocks * ((p.max_len + kTile - 1) / kTile);
   const size_t smem = ((size_t)p.B + 1) * 4;
+  // Short sequences take one launch, with nothing left to a join. With as many sequence-heads
+  // as SMs whole ones fill the GPU (64 sequences of 4 kv heads, 512 slots: 15.1 us, 19.5 split;
+  // 8 kv heads, 256 slots: 16.9, 18.5); with few, a CTA would walk through its tiles alone (one
+  // sequence of 8 kv heads, 200 slots: 8.2 us whole, 6.7 split and joined) and a cluster shares
+  // them (6.2 us, and 2 us less of the host's time than two launches), unless there is one tile
+  // (64 slots: 5.1 us whole, 6.2 split). Clusters beyond what is resident at once would queue:
+  // those are split (8 sequences, 256 slots: 7.7 us; whole 8.5).
+  a.split = PagedSplit::kRanges;
+  if (!p.mass_out && p.max_len <= kWholeLen) {
+    const int64_t pairs = sequence_heads(a);
+    if (pairs >= device_info().sm_count || p.max_len <= kTile) a.split = PagedSplit::kWhole;
+    else if (c.dtype == DD_BF16 && pairs * kPairCtas <= 2 * device_info().sm_count) a.split = PagedSplit::kCluster;
+  }
+  const int64_t units = a.split == PagedSplit::kWhole ? sequence_heads(a) : tiles;
   cudaError_t err;
   if (c.dtype == DD_BF16)
-    err = c.d == 128 ? launch_bf16<128>(a, tiles, smem, stream) : launch_bf16<64>(a, tiles, smem, stream);
+    err = c.d == 128 ? launch_bf16<128>(a, units, smem, stream) : launch_bf16<64>(a, units, smem, stream);
   else
-    err = c.d == 128 ? launch_simt<float, 128>(a, tiles, smem, stream) : launch_simt<float, 64>(a, tiles, smem, stream);
-  if (err != cudaSuccess) return err;
+    err = c.d == 128 ? launch_simt<float, 128>(a, units, smem, stream) : launch_simt<float, 64>(a, units, smem, stream);
+  if (err != cudaSuccess || a.split != PagedSplit::kRanges) return err;
   // join: a CTA per query head; masses: enough CTAs a sequence to fill the GPU a few times
   int mass_ctas = 0;
   if (p.mass_out) {
