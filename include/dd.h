@@ -426,7 +426,7 @@ typedef struct {
  * Errors: DD_ERR_INVALID_ARG for null required pointers, non-positive sizes, Hq % Hkv,
  * misalignment, one of k_new / v_new, max_len or mass_stride out of range, a short
  * workspace; DD_ERR_UNSUPPORTED for d not in {64,128}, B > 4096, Hq > 8192,
- * max_len > 2^30, or 2^31 or more tiles of 64 slots in B * Hq * max_len.
+ * max_len > 2^30, or 2^31 or more tiles of 32 slots in B * Hq * max_len.
  */
 dd_status dd_paged_attention(
     const void* q, int64_t q_stride, const void* k_new, const void* v_new, int64_t new_stride,

@@ -4,7 +4,7 @@
 // partition of the slots is joined from each part's maximum m, sum l = sum e^{s - m}
 // and o = sum e^{s - m} v: m' = max m_i, l' = sum l_i e^{m_i - m'}, o' likewise.
 //
-// Work decomposition. The unit is a tile of 64 slots of one (sequence, kv head, block of
+// Work decomposition. The unit is a tile of 64 slots (32 of 128 fp32 elements) of one (sequence, kv head, block of
 // query heads); the tiles of all of them form one index space, cut into equal contiguous
 // ranges, one per CTA. So ragged batches, one long sequence and many short ones all
 // spread evenly, and a range crosses at most from the end of one sequence-head through
@@ -16,6 +16,8 @@
 // Bound: HBM, 2 Hkv d elements per slot read once.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "dd_paged.cuh"
 #include "dd_tc.cuh"
 
@@ -23,7 +25,8 @@ namespace dd {
 
 namespace {
 
-constexpr int kTile = 64;        // slots per tile
+constexpr int kTileBytes = 32768;  // K and V of a tile of one head, at most
+constexpr int kTileSlots = 64;     // slots of a tile (32 where a row has 512 bytes)
 constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kMaxPagedGrid = 1024;  // bounds the workspace on any device
@@ -66,8 +69,11 @@ struct PagedArgs {
 struct Share {
   int u0, u1;
 };
+__host__ __device__ constexpr int tile_count(int len, int tile) { return (len + tile - 1) / tile; }
+
 // First tile of every sequence into smem prefix[0 .. B] (and CTA 0: the workspace, for
 // the join), and this CTA's share of the tiles.
+template <int TILE>
 __device__ Share plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) {
   const int per_tile = a.c.Hkv * a.blocks;
   const int chunk = (a.B + kPagedThreads - 1) / kPagedThreads;
@@ -76,7 +82,7 @@ __device__ Share plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) 
   for (int b = b0; b < b1; ++b) {
     const int n = checked_length(a.lengths, b, a.max_len);
     prefix[b] = sum;
-    sum += (n + kTile - 1) / kTile * per_tile;
+    sum += tile_count(n, TILE) * per_tile;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = sum;
@@ -104,9 +110,9 @@ __device__ Share plan_tiles(const PagedArgs& a, int32_t* prefix, int* warp_tmp) 
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b <= a.B; b += kPagedThreads) a.prefix[b] = prefix[b];
-  const int share = (prefix[a.B] + a.grid - 1) / a.grid;
-  const int u0 = min(prefix[a.B], (int)blockIdx.x * share);
-  return Share{u0, min(prefix[a.B], u0 + share)};
+  const int64_t total = prefix[a.B], share = (total + a.grid - 1) / a.grid;
+  const int64_t u0 = min(total, blockIdx.x * share);
+  return Share{(int)u0, (int)min(total, u0 + share)};
 }
 
 // The sequence that tile u belongs to: prefix[b] <= u < prefix[b + 1].
@@ -134,220 +140,288 @@ __device__ void write_empty_rows(const PagedArgs& a, const int32_t* prefix, int 
   }
 }
 
-// ------------------------------------------------------------------ CUDA-core form
-template <typename T, int N>
-struct LaneRow {
-  float v[N];
-};
-template <int N>
-__device__ __forceinline__ LaneRow<float, N> load_vec(const float* p) {
-  LaneRow<float, N> r;
-  if constexpr (N == 4) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    r.v[0] = x.x; r.v[1] = x.y; r.v[2] = x.z; r.v[3] = x.w;
-  } else {
-    const float2 x = *reinterpret_cast<const float2*>(p);
-    r.v[0] = x.x; r.v[1] = x.y;
-  }
-  return r;
-}
-template <int N>
-__device__ __forceinline__ LaneRow<__nv_bfloat16, N> load_vec(const __nv_bfloat16* p) {
-  LaneRow<__nv_bfloat16, N> r;
-  if constexpr (N == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    r.v[0] = bf16lo(x.x); r.v[1] = bf16hi(x.x); r.v[2] = bf16lo(x.y); r.v[3] = bf16hi(x.y);
-  } else {
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
-    r.v[0] = bf16lo(x); r.v[1] = bf16hi(x);
-  }
-  return r;
-}
-template <int N>
-__device__ __forceinline__ void store_vec(float* p, const LaneRow<float, N>& x) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) p[e] = x.v[e];
-}
-template <int N>
-__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const LaneRow<__nv_bfloat16, N>& x) {
-#pragma unroll
-  for (int e = 0; e < N; ++e) p[e] = __float2bfloat16_rn(x.v[e]);  // came from bf16: exact
+// ------------------------------------------------------------------ the slots' ring
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Each lane holds d / 32 elements of a row. U slots at a time, a warp forms the U GB
-// partial dot products and sums them over the lanes by halving: after step i a lane
-// keeps the half of the products its lane bit names, so the sums cost U GB - 1 exchanges
-// rather than 5 U GB, and the product of (slot u, head g) ends in the lanes whose top
-// bits are u GB + g. Softmax and mass scores are then one value per lane.
-template <typename T, int D, int GB>
-__global__ void __launch_bounds__(kPagedThreads)
-paged_simt_kernel(const __grid_constant__ PagedArgs a) {
-  constexpr int N = D / 32;
-  constexpr int U = GB >= 8 ? 4 : 8;  // slots in flight per warp
-  constexpr int C = U * GB;           // 8 .. 32
-  constexpr int SH = C == 32 ? 0 : C == 16 ? 1 : 2;
-  extern __shared__ int32_t prefix[];
-  __shared__ int warp_tmp[kPagedWarps];
-  __shared__ float s_m[kPagedWarps][GB], s_l[kPagedWarps][GB];
-  __shared__ float s_o[kPagedWarps][GB][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  pdl_wait();
-  const Share share = plan_tiles(a, prefix, warp_tmp);
-  write_empty_rows<T>(a, prefix, D);
-  int u = share.u0;
-  const int u_end = share.u1;
-  while (u < u_end) {
-    const int b = find_sequence(prefix, a.B, u);
-    const int len = checked_length(a.lengths, b, a.max_len);
-    const int tiles = (len + kTile - 1) / kTile;
+// A place in the tile space: tile `tile` of (sequence b, pair = kv head and head block).
+template <int TILE>
+struct Cursor {
+  int b, len, tiles, pair, tile;
+  __device__ __forceinline__ void enter(const PagedArgs& a, int at) {
+    b = at;
+    len = checked_length(a.lengths, b, a.max_len);
+    tiles = tile_count(len, TILE);
+  }
+  __device__ __forceinline__ void seek(const PagedArgs& a, const int32_t* prefix, int u) {
+    enter(a, find_sequence(prefix, a.B, u));
     const int rel = u - prefix[b];
-    const int pair = rel / tiles, tile0 = rel - pair * tiles;
-    const int n_tiles = min(tiles - tile0, u_end - u);
-    const int kvh = pair / a.blocks, blk = pair - kvh * a.blocks;
-    const int h0 = kvh * a.G + blk * a.heads;          // first query head of the block
-    const int nh = min(a.heads, a.G - blk * a.heads);  // heads of this block
-    const int j0 = tile0 * kTile, j1 = min(len, (tile0 + n_tiles) * kTile);
-    const int32_t* row = a.c.table + (int64_t)b * a.c.table_stride;
-    const int64_t head_off = (int64_t)kvh * a.c.head_bytes;
+    pair = rel / tiles;
+    tile = rel - pair * tiles;
+  }
+  // The next tile; u is its index, below the total.
+  __device__ __forceinline__ void next(const PagedArgs& a, const int32_t* prefix, int u) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++pair < a.c.Hkv * a.blocks) return;
+    pair = 0;
+    int n = b + 1;
+    while (prefix[n + 1] <= u) ++n;  // sequences without slots
+    enter(a, n);
+  }
+};
 
-    float q[GB][N];
-#pragma unroll
-    for (int g = 0; g < GB; ++g) {
-      const T* qp = reinterpret_cast<const T*>(a.q + (int64_t)b * a.q_bytes) +
-                    (int64_t)(h0 + min(g, nh - 1)) * D + lane * N;
-      const auto x = load_vec<N>(qp);
-#pragma unroll
-      for (int e = 0; e < N; ++e) q[g][e] = x.v[e] * a.scale2;
-    }
-    float m = -INFINITY, l = 0.f;  // of head (lane >> SH) % GB
-    float o[GB][N];
-#pragma unroll
-    for (int g = 0; g < GB; ++g)
-#pragma unroll
-      for (int e = 0; e < N; ++e) o[g][e] = 0.f;
+// A warp's slots, SLOTS of each tile of its CTA's range, through S stages of shared memory
+// (cp.async; K, then V, a group each), on and on across sequence-heads: warps wait for one
+// another only where a sequence-head ends. Rows are swizzled by 16-byte chunks (chunk c of
+// row r at c ^ (r % 8)). Page ids are fetched one tile ahead of the copies that need them.
+// Slots in holes or behind the end arrive as zeros.
+template <int ROW, int SLOTS, int S>
+struct SlotRing {
+  static constexpr int kTile = kPagedWarps * SLOTS;
+  static constexpr int kHalf = SLOTS * ROW;  // K, or V, of one stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kBytes = kPagedWarps * S * kStage;
+  static constexpr int CH = ROW / 16;        // chunks of a row
+  static constexpr int RPI = 32 / CH;        // rows a warp copies per instruction
+  static_assert(S * SLOTS <= 64 && kTile * ROW * 2 <= kTileBytes);
 
-    for (int j = j0 + warp * U; j < j1; j += kPagedWarps * U) {
-      LaneRow<T, N> kr[U], vr[U];
-      unsigned held = 0;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t off = j + i < j1 ? slot_offset(a.c, row, j + i) : -1;
-#pragma unroll
-        for (int e = 0; e < N; ++e) kr[i].v[e] = vr[i].v[e] = 0.f;
-        if (off < 0) continue;
-        held |= 1u << i;
-        T* kp = reinterpret_cast<T*>(a.c.k + off + head_off) + lane * N;
-        T* vp = reinterpret_cast<T*>(a.c.v + off + head_off) + lane * N;
-        if (a.k_new && j + i == len - 1) {  // the new token: read from the caller, kept in the cache
-          const int64_t at = (int64_t)b * a.new_bytes;
-          kr[i] = load_vec<N>(reinterpret_cast<const T*>(a.k_new + at) + kvh * D + lane * N);
-          vr[i] = load_vec<N>(reinterpret_cast<const T*>(a.v_new + at) + kvh * D + lane * N);
-          if (blk == 0) {
-            store_vec<N>(kp, kr[i]);
-            store_vec<N>(vp, vr[i]);
-          }
-        } else {
-          kr[i] = load_vec<N>(kp);
-          vr[i] = load_vec<N>(vp);
-        }
-      }
-      float s[C];
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int g = 0; g < GB; ++g) {
-          float t = 0.f;
-#pragma unroll
-          for (int e = 0; e < N; ++e) t = fmaf(q[g][e], kr[i].v[e], t);
-          s[i * GB + g] = t;
-        }
-      int n = C;
-#pragma unroll
-      for (int bit = 16; bit > 0; bit >>= 1) {
-        if (n > 1) {
-          n >>= 1;
-          const bool up = lane & bit;
-#pragma unroll
-          for (int i = 0; i < C / 2; ++i)
-            if (i < n) {
-              const float mine = up ? s[i + n] : s[i], give = up ? s[i] : s[i + n];
-              s[i] = mine + __shfl_xor_sync(0xffffffffu, give, bit);
-            }
-        } else {
-          s[0] += __shfl_xor_sync(0xffffffffu, s[0], bit);
-        }
-      }
-      const int c = lane >> SH, iu = c / GB, ig = c % GB;
-      const float sc = (held >> iu) & 1u ? s[0] : -INFINITY;
-      if (a.scores && (lane & ((1 << SH) - 1)) == 0 && ig < nh && j + iu < j1)
-        a.scores[((int64_t)b * a.Hq + h0 + ig) * a.score_row + j + iu] = sc;
-      float mx = sc;
-#pragma unroll
-      for (int bit = 16; bit >= 32 / U; bit >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, bit));
-      const float m_new = fmaxf(m, mx);
-      const float base = m_new == -INFINITY ? 0.f : m_new;
-      const float p = exp2f(sc - base);
-      const float alpha = exp2f(m - base);
-      float ps = p;
-#pragma unroll
-      for (int bit = 16; bit >= 32 / U; bit >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, bit);
-      l = l * alpha + ps;
-      m = m_new;
-#pragma unroll
-      for (int g = 0; g < GB; ++g) {
-        const float al = __shfl_sync(0xffffffffu, alpha, g << SH);
-#pragma unroll
-        for (int e = 0; e < N; ++e) o[g][e] *= al;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const float pi = __shfl_sync(0xffffffffu, p, (i * GB + g) << SH);
-#pragma unroll
-          for (int e = 0; e < N; ++e) o[g][e] = fmaf(pi, vr[i].v[e], o[g][e]);
-        }
-      }
-    }
-    // ---- join the four warps
-    __syncthreads();  // the previous piece's reads of s_* are over
-    if (lane < (GB << SH) && (lane & ((1 << SH) - 1)) == 0) {
-      s_m[warp][lane >> SH] = m;
-      s_l[warp][lane >> SH] = l;
+  const PagedArgs& a;
+  const int32_t* prefix;
+  int64_t* new_at;  // [S] where a stage's new token goes
+  uint32_t ring;
+  int lane, warp, lu, u_end, id;
+  uint64_t held_q;  // SLOTS bits per stage: slots that count
+  Cursor<kTile> lc;  // the tile whose page ids are held
+
+  __device__ __forceinline__ SlotRing(const PagedArgs& args, const int32_t* pre, uint8_t* smem, int64_t* s_new,
+                                      int u0, int u1)
+      : a(args), prefix(pre), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), lu(u0), u_end(u1), id(-1), held_q(0) {
+    new_at = s_new + warp * S;
+    ring = smem_u32(smem) + warp * (S * kStage);
+    if (u0 < u1) {
+      lc.seek(a, prefix, u0);
+      fetch_id();
     }
 #pragma unroll
-    for (int g = 0; g < GB; ++g)
+    for (int s = 0; s < S - 1; ++s) issue(s);
+  }
+  __device__ __forceinline__ int slot() const { return lc.tile * kTile + warp * SLOTS + lane % SLOTS; }
+  __device__ __forceinline__ void fetch_id() {
+    id = slot() < lc.len ? a.c.table[(int64_t)lc.b * a.c.table_stride + div_fast(a.c.page, slot())] : -1;
+  }
+  // The queries of a sequence-head are read when its tiles come up: into L2 before that.
+  __device__ __forceinline__ void prefetch_q() const {
+    const int kvh = lc.pair / a.blocks, blk = lc.pair - kvh * a.blocks;
+    const char* q = a.q + (int64_t)lc.b * a.q_bytes + (int64_t)(kvh * a.G + blk * a.heads) * ROW;
+    for (int x = lane; x < min(a.heads, a.G - blk * a.heads) * (ROW / 128); x += 32) prefetch_l2(q + x * 128);
+  }
+  // Whether slot r of a stage counts.
+  __device__ __forceinline__ uint32_t held(int stage) const {
+    return (uint32_t)(held_q >> (SLOTS * stage)) & ((1u << SLOTS) - 1u);
+  }
+  __device__ __forceinline__ uint32_t k_at(int stage) const { return ring + stage * kStage; }
+  __device__ __forceinline__ uint32_t v_at(int stage) const { return ring + stage * kStage + kHalf; }
+  static __device__ __forceinline__ uint32_t chunk(int r, int c) { return r * ROW + ((c ^ (r & 7)) << 4); }
+
+  // Start the copies of the next tile (or of nothing: empty groups keep the count).
+  __device__ __forceinline__ void issue(int stage) {
+    if (lu >= u_end) {
+      cp_async_commit();
+      cp_async_commit();
+      return;
+    }
+    constexpr uint32_t kAll = (1u << SLOTS) - 1u;
+    const int j = slot(), kvh = lc.pair / a.blocks;
+    const int page = checked_page(id, a.c.n_pages);
+    const bool ok = page >= 0;  // j < len is in the id
+    int64_t off = 0;
+    if (ok)
+      off = (int64_t)page * a.c.page_bytes + (int64_t)kvh * a.c.head_bytes +
+            (int64_t)(j - div_fast(a.c.page, j) * a.c.page.n) * a.c.token_bytes;
+    const uint32_t rows = __ballot_sync(0xffffffffu, ok) & kAll;
+    const uint32_t fresh = __ballot_sync(0xffffffffu, ok && a.k_new && j == lc.len - 1) & kAll;
+    held_q = (held_q & ~((uint64_t)kAll << (SLOTS * stage))) | ((uint64_t)rows << (SLOTS * stage));
+    if ((fresh >> (lane % SLOTS)) & 1u) new_at[stage] = off;  // the slot's lanes: the same
+    const uint32_t dst = k_at(stage);
+    const int c = lane % CH, r0 = lane / CH;
+    if (a.even_pages && !fresh) {  // the rows are of one page: one address and a stride
+      const int64_t o = __shfl_sync(0xffffffffu, off, 0) + r0 * a.c.token_bytes + c * 16;
 #pragma unroll
-      for (int e = 0; e < N; ++e) s_o[warp][g][lane * N + e] = o[g][e];
-    __syncthreads();
-    const bool starts = tile0 == 0, whole = starts && n_tiles == tiles;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
-    for (int i = threadIdx.x; i < nh * D; i += kPagedThreads) {
-      const int g = i / D, e = i - g * D;
-      float mm = s_m[0][g];
+      for (int kv = 0; kv < 2; ++kv) {
+        const char* src = (kv ? a.c.v : a.c.k) + o;
 #pragma unroll
-      for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f, oo = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) {
-        const float f = exp2f(s_m[w][g] - base);
-        ll = fmaf(s_l[w][g], f, ll);
-        oo = fmaf(s_o[w][g][e], f, oo);
-      }
-      if (whole) {
-        const int64_t h = (int64_t)b * a.Hq + h0 + g;
-        store_out(reinterpret_cast<T*>(a.out) + h * D + e, ll > 0.f ? oo / ll : 0.f);
-        if (e == 0) {
-          const float z2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
-          a.lse2[h] = z2;
-          if (a.lse) a.lse[h] = z2 * kLn2;
+        for (int i = 0; i < SLOTS / RPI; ++i) {
+          const int r = i * RPI + r0;
+          cp_async16(dst + kv * kHalf + chunk(r, c), src, (rows >> r) & 1u ? 16 : 0);
+          src += RPI * a.c.token_bytes;
         }
-      } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
-        a.part_o[(slot * a.heads + g) * D + e] = oo;
-        if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
+        cp_async_commit();
+      }
+    } else {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const char* base = kv ? a.c.v : a.c.k;
+#pragma unroll
+        for (int i = 0; i < SLOTS / RPI; ++i) {
+          const int r = i * RPI + r0;
+          const char* src = base + __shfl_sync(0xffffffffu, off, r);
+          if ((fresh >> r) & 1u)  // the new token: read from the caller
+            src = (kv ? a.v_new : a.k_new) + (int64_t)lc.b * a.new_bytes + kvh * ROW;
+          cp_async16(dst + kv * kHalf + chunk(r, c), src + c * 16, (rows >> r) & 1u ? 16 : 0);
+        }
+        cp_async_commit();
       }
     }
-    u += n_tiles;
+    if (++lu < u_end) {
+      lc.next(a, prefix, lu);
+      fetch_id();
+      if (lc.tile == 0 && warp == 0) prefetch_q();
+    }
+  }
+  // The new token, from its row of a stage, into the cache.
+  __device__ __forceinline__ void keep_new(int stage, int r) const {
+    const int64_t to = new_at[stage] + (lane % CH) * 16;
+    if (lane >= CH) return;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4 w;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                   : "r"(k_at(stage) + kv * kHalf + chunk(r, lane % CH)) : "memory");
+      *reinterpret_cast<uint4*>((kv ? a.c.v : a.c.k) + to) = w;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ the end of a sequence-head
+__device__ __forceinline__ void store4(float* p, const float4& x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& x) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(x.x, x.y), tc::pack_bf16(x.z, x.w));
+}
+__device__ __forceinline__ void add_scaled(float4& o, const float4& x, float f) {
+  o.x = fmaf(x.x, f, o.x); o.y = fmaf(x.y, f, o.y);
+  o.z = fmaf(x.z, f, o.z); o.w = fmaf(x.w, f, o.w);
+}
+// Head h's output from its sums.
+template <typename T, int D>
+__device__ __forceinline__ void write_out(const PagedArgs& a, int64_t h, int e, float m, float l, float4 o) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  store4(reinterpret_cast<T*>(a.out) + h * D + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (e != 0) return;
+  const float z2 = l > 0.f ? m + log2f(l) : -INFINITY;
+  if (a.scores) a.lse2[h] = z2;
+  if (a.lse) a.lse[h] = z2 * kLn2;
+}
+
+// A cluster's CTA results: (m, l) per head and [head][d], where its joined results go.
+template <int H>
+struct ClusterPart {
+  float m[H], l[H];
+};
+
+// A piece: the tiles of one sequence-head a CTA has.
+struct Piece {
+  int b, h0, heads;      // sequence, first query head, heads
+  bool starts, whole;    // it has the head's first tile; all of them
+};
+
+// Join the four warps' results of up to 8 heads, heads t0 .. of the piece: joined(w) is warp
+// w's [8][D], element e of a row at e ^ (8 * (head / 2 % 4)) (which spreads the heads that
+// lanes write at once over the banks), s_m / s_l its maxima and sums. Whole sequence-heads
+// are written out; a cluster's CTA keeps its part; else it goes to the workspace.
+template <typename T, int D, int H, bool CL, typename J>
+__device__ __forceinline__ void join_warps(const PagedArgs& a, const Piece& p, int t0, const float (*s_m)[H],
+                                           const float (*s_l)[H], J joined, ClusterPart<CL ? H : 1>& part,
+                                           float* part_o) {
+  const int64_t slot = 2 * (int64_t)blockIdx.x + (p.starts ? 1 : 0);
+  for (int i = threadIdx.x; i < min(p.heads - t0, 8) * (D / 4); i += kPagedThreads) {
+    const int gt = i / (D / 4), e = (i - gt * (D / 4)) * 4, g = t0 + gt;
+    float mm = s_m[0][g];
+#pragma unroll
+    for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) {
+      const float f = exp2f(s_m[w][g] - base);
+      ll = fmaf(s_l[w][g], f, ll);
+      add_scaled(oo, *reinterpret_cast<const float4*>(joined(w) + gt * D + (e ^ (((gt >> 1) & 3) << 3))), f);
+    }
+    if constexpr (CL) {
+      *reinterpret_cast<float4*>(part_o + gt * D + e) = oo;
+      if (e == 0) { part.m[g] = mm; part.l[g] = ll; }
+    } else if (p.whole) {
+      write_out<T, D>(a, (int64_t)p.b * a.Hq + p.h0 + g, e, mm, ll, oo);
+    } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
+      *reinterpret_cast<float4*>(a.part_o + (slot * a.heads + g) * D + e) = oo;
+      if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
+    }
   }
 }
+
+// Cluster launches: this CTA's share of a sequence-head's tiles. Returns false where the
+// sequence has no slots.
+template <int TILE>
+__device__ __forceinline__ bool cluster_share(const PagedArgs& a, const int32_t* prefix, int& b, int& pair, Share& share) {
+  const int per = a.c.Hkv * a.blocks, p = blockIdx.x / kPairCtas, rank = blockIdx.x - p * kPairCtas;
+  b = p / per;
+  pair = p - b * per;
+  const int tiles = (prefix[b + 1] - prefix[b]) / per;
+  const int each = tile_count(tiles, kPairCtas), first = prefix[b] + pair * tiles;
+  share = Share{first + min(tiles, rank * each), first + min(tiles, (rank + 1) * each)};
+  return tiles > 0;
+}
+// The cluster's CTAs join their parts, an eighth of the elements each. part_at(g): head g's
+// row of the CTA's own shared memory.
+template <typename T, int D, int H, typename P>
+__device__ __forceinline__ void join_cluster(const PagedArgs& a, int b, int pair, bool has_part, ClusterPart<H>& part,
+                                             P part_at) {
+  namespace cg = cooperative_groups;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int kvh = pair / a.blocks, blk = pair - kvh * a.blocks;
+  const int h0 = kvh * a.G + blk * a.heads, nh = min(a.heads, a.G - blk * a.heads);
+  if (!has_part && threadIdx.x < H) { part.m[threadIdx.x] = -INFINITY; part.l[threadIdx.x] = 0.f; }
+  cluster.sync();
+  for (int i = (int)cluster.block_rank() * kPagedThreads + threadIdx.x; i < nh * (D / 4); i += kPairCtas * kPagedThreads) {
+    const int g = i / (D / 4), e = (i - g * (D / 4)) * 4;
+    float mr[kPairCtas], lr[kPairCtas];
+    float4 x[kPairCtas];
+#pragma unroll
+    for (int r = 0; r < kPairCtas; ++r) {
+      mr[r] = *cluster.map_shared_rank(&part.m[g], r);
+      lr[r] = *cluster.map_shared_rank(&part.l[g], r);
+      x[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(part_at(g) + e, r));
+    }
+    float mm = mr[0];
+#pragma unroll
+    for (int r = 1; r < kPairCtas; ++r) mm = fmaxf(mm, mr[r]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kPairCtas; ++r) {
+      if (mr[r] == -INFINITY) continue;  // its shared memory may hold no result
+      const float f = exp2f(mr[r] - base);
+      ll = fmaf(lr[r], f, ll);
+      add_scaled(oo, x[r], f);
+    }
+    write_out<T, D>(a, (int64_t)b * a.Hq + h0 + g, e, mm, ll, oo);
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// Shapes of a kernel: slots of a warp's stage (8 KB of K and V, or less), stages, CTAs an SM.
+template <typename T, int D, int S_, int CTAS>
+struct PagedCfg {
+  static constexpr int S = S_, kCtas = CTAS;
+  static constexpr int ROW = D * (int)sizeof(T);
+  static constexpr int SLOTS = ROW == 512 ? 8 : 16;
+  using Ring = SlotRing<ROW, SLOTS, S>;
+  static constexpr int kSmem = Ring::kBytes;
+  static_assert(8 * D * 4 <= Ring::kHalf);  // a warp's results, in the place of a stage's K
+};
 
 // ------------------------------------------------------------------ tensor-core form (bf16)
 // Per warp and tile: 16 slots. S^T [16 slots x heads] = K Q^T and O^T [d x heads] += V^T P^T
@@ -358,14 +432,6 @@ paged_simt_kernel(const __grid_constant__ PagedArgs a) {
 // slots before its first product, where a warp's 16 slots start as they arrive.
 // P is carried as two bf16 terms (16 bits of a weight), so the output has fp32 weights'
 // accuracy; one term alone would add as much error again as the output's own rounding.
-// Each warp streams its own slots through a ring of stages in shared memory (cp.async,
-// rows swizzled by 16-byte chunks) that runs on across tiles and sequences; page ids are
-// fetched one tile ahead of the copies that need them. Warps meet only to join a
-// sequence-head's results.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -386,191 +452,58 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A place in the tile space: tile `tile` of (sequence b, pair = kv head and head block).
-struct Cursor {
-  int b, len, tiles, pair, tile;
-  __device__ __forceinline__ void enter(const PagedArgs& a, const int32_t* prefix, int at) {
-    b = at;
-    len = checked_length(a.lengths, b, a.max_len);
-    tiles = (len + kTile - 1) / kTile;
-  }
-  __device__ __forceinline__ void seek(const PagedArgs& a, const int32_t* prefix, int u) {
-    enter(a, prefix, find_sequence(prefix, a.B, u));
-    const int rel = u - prefix[b];
-    pair = rel / tiles;
-    tile = rel - pair * tiles;
-  }
-  // The next tile; u is its index, below the total.
-  __device__ __forceinline__ void next(const PagedArgs& a, const int32_t* prefix, int u) {
-    if (++tile < tiles) return;
-    tile = 0;
-    if (++pair < a.c.Hkv * a.blocks) return;
-    pair = 0;
-    int n = b + 1;
-    while (prefix[n + 1] <= u) ++n;  // sequences without slots
-    enter(a, prefix, n);
-  }
-};
-
-constexpr int kWarpSlots = 16;  // slots of a tile per warp
-
-// Stages of a warp's ring. Two CTAs an SM with three stages keep the most bytes in flight,
-// which one long sequence wants (131071 slots, 8 kv heads: 88.7 us, against 92.9 with three
-// CTAs of two stages). Where there are as many sequence-heads as SMs their ends and starts
-// cost more, and a third CTA works through them (7 sequences of 32 kv heads: 26.9 us against
-// 29.0; 64 of 4: 109.5 against 111.0).
-template <int D, int NT, int S>
-struct MmaCfg {
-  static constexpr int kStages = S;
-  static constexpr int kCtas = S == 2 && NT == 1 ? 3 : 2;  // per SM
-  static constexpr int kRowBytes = D * 2;
-  static constexpr int kHalf = kWarpSlots * kRowBytes;  // K, or V, of one stage
-  static constexpr int kSmem = kPagedWarps * kStages * 2 * kHalf;
-  static_assert(8 * D * 4 <= kHalf);  // results at the end of a sequence-head
-};
-
-// CL: a cluster of kPairCtas CTAs for each sequence-head, its tiles split among them, their
-// results joined through distributed shared memory: one launch, for few short sequences,
-// where the latency of the call is what counts.
-template <int D, int NT, int S, bool CL>
-__global__ void __launch_bounds__(kPagedThreads, MmaCfg<D, NT, S>::kCtas)
+// NT column tiles of 8 query heads. CL: a cluster of kPairCtas CTAs for each sequence-head,
+// its tiles split among them, their results joined through distributed shared memory: one
+// launch, for few short sequences, where the latency of the call is what counts.
+template <typename C, int D, int NT, bool CL>
+__global__ void __launch_bounds__(kPagedThreads, C::kCtas)
 paged_mma_kernel(const __grid_constant__ PagedArgs a) {
-  using C = MmaCfg<D, NT, S>;
-  constexpr int H = NT * 8;       // heads, padded
-  constexpr int KS = D / 16;      // k-steps of S, row tiles of O
-  constexpr int CH = D / 8;       // 16-byte chunks of a row
-  constexpr int RPI = 32 / CH;    // rows a warp copies per instruction
+  using Ring = typename C::Ring;
+  constexpr int H = NT * 8, KS = D / 16;  // heads, padded; k-steps of S and row tiles of O
+  constexpr int S = C::S, ROW = C::ROW;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int warp_tmp[kPagedWarps];
   __shared__ float s_m[kPagedWarps][H], s_l[kPagedWarps][H];
-  __shared__ int64_t s_new[kPagedWarps][C::kStages];  // where a stage's new token goes
+  __shared__ int64_t s_new[kPagedWarps * S];
+  __shared__ ClusterPart<CL ? H : 1> part;
   int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  Share share = plan_tiles(a, prefix, warp_tmp);
+  Share share = plan_tiles<Ring::kTile>(a, prefix, warp_tmp);
   write_empty_rows<__nv_bfloat16>(a, prefix, D);
-  // CL: the cluster's sequence and head, and this CTA's results, [head][d] in the V parts of
-  // the first stages of warps 0 (heads 0 - 7) and 1, which nobody reads any more by then
   [[maybe_unused]] int cl_b = 0, cl_pair = 0;
-  __shared__ float cl_m[CL ? H : 1], cl_l[CL ? H : 1];
-  [[maybe_unused]] const auto cl_at = [](int g, int e) {
-    return (g / 8) * (C::kStages * 2 * C::kHalf) + C::kHalf + ((g % 8) * D + e) * 4;
+  // a cluster's part goes to the V of the first stages of warps 0 (heads 0 - 7) and 1, which
+  // nobody reads any more by then
+  const auto part_at = [&](int g) {
+    return reinterpret_cast<float*>(smem + (g / 8) * (S * Ring::kStage) + Ring::kHalf) + (g % 8) * D;
   };
   if constexpr (CL) {
-    const int per = a.c.Hkv * a.blocks, p = blockIdx.x / kPairCtas, rank = blockIdx.x - p * kPairCtas;
-    cl_b = p / per;
-    cl_pair = p - cl_b * per;
-    const int tiles = (prefix[cl_b + 1] - prefix[cl_b]) / per;
-    if (tiles == 0) return;  // the whole cluster
-    const int each = (tiles + kPairCtas - 1) / kPairCtas, first = prefix[cl_b] + cl_pair * tiles;
-    share = Share{first + min(tiles, rank * each), first + min(tiles, (rank + 1) * each)};
+    if (!cluster_share<Ring::kTile>(a, prefix, cl_b, cl_pair, share)) return;  // the whole cluster
+  } else if (share.u0 >= share.u1) {
+    return;
   }
-  const int u0 = share.u0, u_end = share.u1;
-  if (!CL && u0 >= u_end) return;
-  const uint32_t ring = smem_u32(smem) + warp * (C::kStages * 2 * C::kHalf);
-
-  // ---- copies: the page id of this lane's slot one tile ahead, then the rows
-  Cursor lc;  // the tile whose page ids are held
-  if (!CL || u0 < u_end) lc.seek(a, prefix, u0);
-  int lu = u0;
-  int id = -1;
-  const auto fetch_id = [&]() {
-    const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
-    id = j < lc.len ? a.c.table[(int64_t)lc.b * a.c.table_stride + div_fast(a.c.page, j)] : -1;
-  };
-  // the queries of a sequence-head are read when its tiles come up: into L2 before that
-  const auto prefetch_q = [&](const Cursor& x) {
-    const int kvh = x.pair / a.blocks, blk = x.pair - kvh * a.blocks;
-    const int lines = min(a.heads, a.G - blk * a.heads) * (C::kRowBytes / 128);
-    if (lane < lines)
-      prefetch_l2(a.q + (int64_t)x.b * a.q_bytes + (int64_t)(kvh * a.G + blk * a.heads) * C::kRowBytes + lane * 128);
-  };
-  if (!CL || u0 < u_end) fetch_id();
-  uint64_t held_q = 0;  // 16 bits per stage: slots that count
-  const auto issue = [&](int stage) {
-    if (lu < u_end) {
-      const int j = lc.tile * kTile + warp * kWarpSlots + (lane & 15);
-      const int kvh = lc.pair / a.blocks;
-      const int page = checked_page(id, a.c.n_pages);
-      const bool ok = page >= 0;  // j < len is in the id
-      int64_t off = 0;
-      if (ok)
-        off = (int64_t)page * a.c.page_bytes + (int64_t)kvh * a.c.head_bytes +
-              (int64_t)(j - div_fast(a.c.page, j) * a.c.page.n) * a.c.token_bytes;
-      const uint32_t held = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      const uint32_t fresh = __ballot_sync(0xffffffffu, ok && a.k_new && j == lc.len - 1) & 0xffffu;
-      held_q = (held_q & ~(0xffffull << (16 * stage))) | ((uint64_t)held << (16 * stage));
-      if ((fresh >> (lane & 15)) & 1u) s_new[warp][stage] = off;  // both lanes of the slot: the same
-      const uint32_t dst = ring + stage * 2 * C::kHalf;
-      const int c = lane % CH, r0 = lane / CH;
-      if (a.even_pages && !fresh) {  // 16 rows of one page: one address and a stride
-        const int64_t o = __shfl_sync(0xffffffffu, off, 0) + r0 * a.c.token_bytes + c * 16;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const char* src = (kv ? a.c.v : a.c.k) + o;
-#pragma unroll
-          for (int i = 0; i < kWarpSlots / RPI; ++i) {
-            const int r = i * RPI + r0;
-            cp_async16(dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4), src, (held >> r) & 1u ? 16 : 0);
-            src += RPI * a.c.token_bytes;
-          }
-          if (kv == 0) cp_async_commit();
-        }
-      } else {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const char* base = kv ? a.c.v : a.c.k;
-#pragma unroll
-          for (int i = 0; i < kWarpSlots / RPI; ++i) {
-            const int r = i * RPI + r0;
-            const char* src = base + __shfl_sync(0xffffffffu, off, r);
-            if ((fresh >> r) & 1u)  // the new token: read from the caller
-              src = (kv ? a.v_new : a.k_new) + (int64_t)lc.b * a.new_bytes + kvh * C::kRowBytes;
-            cp_async16(dst + kv * C::kHalf + r * C::kRowBytes + ((c ^ (r & 7)) << 4), src + c * 16,
-                       (held >> r) & 1u ? 16 : 0);
-          }
-          if (kv == 0) cp_async_commit();
-        }
-      }
-      cp_async_commit();
-      if (++lu < u_end) {
-        lc.next(a, prefix, lu);
-        fetch_id();
-        if (lc.tile == 0 && warp == 0) prefetch_q(lc);
-      }
-    } else {  // empty groups keep the count
-      cp_async_commit();
-      cp_async_commit();
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) issue(s);
-
-  // ---- the products
-  Cursor cc;
-  if (!CL || u0 < u_end) cc.seek(a, prefix, u0);
+  const int u_end = share.u1;
+  Ring ring(a, prefix, smem, s_new, share.u0, u_end);
+  Cursor<Ring::kTile> cc;
+  if (!CL || share.u0 < u_end) cc.seek(a, prefix, share.u0);
   int stage = 0;
-  for (int u = u0; u < u_end;) {
+  for (int u = share.u0; u < u_end;) {
     const int b = cc.b, len = cc.len, tiles = cc.tiles, tile0 = cc.tile;
     const int n_tiles = min(tiles - tile0, u_end - u);
     const int kvh = cc.pair / a.blocks, blk = cc.pair - kvh * a.blocks;
-    const int h0 = kvh * a.G + blk * a.heads;
-    const int nh = min(a.heads, a.G - blk * a.heads);
+    const Piece piece{b, kvh * a.G + blk * a.heads, min(a.heads, a.G - blk * a.heads), tile0 == 0,
+                      n_tiles == tiles};
+    const int h0 = piece.h0, nh = piece.heads;
     // the tile of this piece, if any, whose slots of this warp hold the new token
-    const int new_tile = a.k_new && blk == 0 && ((len - 1) % kTile) / kWarpSlots == warp ? tiles - 1 - tile0 : -1;
-    const int new_row = (len - 1) & (kWarpSlots - 1);
-    const auto row_chunk = [&](uint32_t base, int r) {  // this lane's 16 bytes of a staged row
-      uint4 w;
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                   : "r"(base + r * C::kRowBytes + (((lane % CH) ^ (r & 7)) << 4)) : "memory");
-      return w;
-    };
+    const int new_tile =
+        a.k_new && blk == 0 && ((len - 1) % Ring::kTile) / C::SLOTS == warp ? tiles - 1 - tile0 : -1;
+    const int new_row = (len - 1) % C::SLOTS;
     uint32_t q[NT][KS][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int h = t * 8 + (lane >> 2);
       const uint32_t* qp = reinterpret_cast<const uint32_t*>(
-          a.q + (int64_t)b * a.q_bytes + (int64_t)(h0 + min(h, nh - 1)) * C::kRowBytes) + (lane & 3);
+          a.q + (int64_t)b * a.q_bytes + (int64_t)(h0 + min(h, nh - 1)) * ROW) + (lane & 3);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         q[t][k][0] = h < nh ? qp[k * 8] : 0u;
@@ -590,10 +523,10 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     }
     for (int i = 0; i < n_tiles; ++i) {
       __syncwarp();  // every lane has read the stage that is filled next
-      issue(stage == 0 ? C::kStages - 1 : stage - 1);
-      const uint32_t kb = ring + stage * 2 * C::kHalf, vb = kb + C::kHalf;
-      const uint32_t held = (uint32_t)(held_q >> (16 * stage)) & 0xffffu;
-      cp_async_wait<2 * C::kStages - 1>();
+      ring.issue(stage == 0 ? S - 1 : stage - 1);
+      const uint32_t kb = ring.k_at(stage), vb = ring.v_at(stage);
+      const uint32_t held = ring.held(stage);
+      cp_async_wait<2 * S - 1>();
       __syncwarp();
       float s[NT][4];
 #pragma unroll
@@ -602,7 +535,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t f[4];
-        ldsm4(kb + kr * C::kRowBytes + (((2 * k + (lane >> 4)) ^ (kr & 7)) << 4), f);
+        ldsm4(kb + Ring::chunk(kr, 2 * k + (lane >> 4)), f);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma16816(s[t], f, q[t][k][0], q[t][k][1]);
       }
@@ -614,7 +547,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[t][e] = (e < 2 ? in0 : in1) ? s[t][e] * a.scale2 : -INFINITY;
         if (a.scores) {
-          const int j = (tile0 + i) * kTile + warp * kWarpSlots + (lane >> 2);
+          const int j = (tile0 + i) * Ring::kTile + warp * C::SLOTS + (lane >> 2);
           const int g = t * 8 + 2 * (lane & 3);
           float* sp = a.scores + ((int64_t)b * a.Hq + h0 + g) * a.score_row + j;
           if (g < nh && j < len) sp[0] = s[t][0];
@@ -650,29 +583,22 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
           pl[t][r] = transpose8x8(lo);
         }
       }
-      cp_async_wait<2 * C::kStages - 2>();
+      cp_async_wait<2 * S - 2>();
       __syncwarp();
       const int vr = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t f[4];
-        ldsm4_trans(vb + vr * C::kRowBytes + (((2 * k + ((lane >> 3) & 1)) ^ (vr & 7)) << 4), f);
+        ldsm4_trans(vb + Ring::chunk(vr, 2 * k + ((lane >> 3) & 1)), f);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           mma16816(o[k][t], f, ph[t][0], ph[t][1]);
           mma16816(o[k][t], f, pl[t][0], pl[t][1]);
         }
       }
-      if (i == new_tile && ((held >> new_row) & 1u)) {  // the new token, from its row here, into the cache
-        const int64_t to = s_new[warp][stage] + (lane % CH) * 16;
-        if (lane < CH) {
-          *reinterpret_cast<uint4*>(a.c.k + to) = row_chunk(kb, new_row);
-          *reinterpret_cast<uint4*>(a.c.v + to) = row_chunk(vb, new_row);
-        }
-      }
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      if (i == new_tile && ((held >> new_row) & 1u)) ring.keep_new(stage, new_row);
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    // ---- join the four warps
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -683,16 +609,10 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         l[t][e] = x;
       }
-    // the stage read last is not refilled before the join: its place takes a warp's results,
-    // [8 heads][d] fp32 at a time; element e of a head's row lies at
-    // e ^ (8 * (head / 2 % 4)), which spreads the heads a warp writes at once over the banks
-    const int last = stage == 0 ? C::kStages - 1 : stage - 1;
-    const auto joined = [&](int w) {
-      return reinterpret_cast<float*>(smem + (w * C::kStages + last) * 2 * C::kHalf);
-    };
+    // the stage read last is not refilled before the join: its K takes a warp's results
+    const int last = stage == 0 ? S - 1 : stage - 1;
+    const auto joined = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + last) * Ring::kStage); };
     __syncwarp();
-    const bool starts = tile0 == 0, whole = starts && n_tiles == tiles;
-    const int64_t slot = 2 * (int64_t)blockIdx.x + (starts ? 1 : 0);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (t > 0) __syncthreads();  // the first eight heads' results are read
@@ -712,40 +632,7 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
         }
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < min(nh - t * 8, 8) * (D / 4); i += kPagedThreads) {
-        const int gt = i / (D / 4), e = (i - gt * (D / 4)) * 4, g = t * 8 + gt;
-        float mm = s_m[0][g];
-#pragma unroll
-        for (int w = 1; w < kPagedWarps; ++w) mm = fmaxf(mm, s_m[w][g]);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f;
-        float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kPagedWarps; ++w) {
-          const float f = exp2f(s_m[w][g] - base);
-          ll = fmaf(s_l[w][g], f, ll);
-          const float4 x = *reinterpret_cast<const float4*>(joined(w) + gt * D + (e ^ (((gt >> 1) & 3) << 3)));
-          oo.x = fmaf(x.x, f, oo.x); oo.y = fmaf(x.y, f, oo.y);
-          oo.z = fmaf(x.z, f, oo.z); oo.w = fmaf(x.w, f, oo.w);
-        }
-        if constexpr (CL) {  // kept for the cluster
-          *reinterpret_cast<float4*>(smem + cl_at(g, e)) = oo;
-          if (e == 0) { cl_m[g] = mm; cl_l[g] = ll; }
-        } else if (whole) {
-          const int64_t h = (int64_t)b * a.Hq + h0 + g;
-          const float inv = ll > 0.f ? 1.f / ll : 0.f;
-          const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
-          *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
-          if (e == 0) {
-            const float z2 = ll > 0.f ? mm + log2f(ll) : -INFINITY;
-            a.lse2[h] = z2;
-            if (a.lse) a.lse[h] = z2 * kLn2;
-          }
-        } else if (DD_IN_BOUNDS(slot < 2ll * a.grid)) {
-          *reinterpret_cast<float4*>(a.part_o + (slot * a.heads + g) * D + e) = oo;
-          if (e == 0) a.part_ml[slot * a.heads + g] = make_float2(mm, ll);
-        }
-      }
+      join_warps<__nv_bfloat16, D, H, CL>(a, piece, t * 8, s_m, s_l, joined, part, part_at(t * 8));
     }
     u += n_tiles;
     if (!CL && u < u_end) {
@@ -754,46 +641,200 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
       cc.next(a, prefix, u);
     }
   }
-  if constexpr (CL) {
-    namespace cg = cooperative_groups;
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int kvh = cl_pair / a.blocks, blk = cl_pair - kvh * a.blocks;
-    const int h0 = kvh * a.G + blk * a.heads, nh = min(a.heads, a.G - blk * a.heads);
-    if (u0 == u_end && threadIdx.x < H) { cl_m[threadIdx.x] = -INFINITY; cl_l[threadIdx.x] = 0.f; }
-    cluster.sync();
-    const int rank = (int)cluster.block_rank();
-    for (int i = rank * kPagedThreads + threadIdx.x; i < nh * (D / 4); i += kPairCtas * kPagedThreads) {
-      const int g = i / (D / 4), e = (i - g * (D / 4)) * 4;
-      float mr[kPairCtas], lr[kPairCtas];
-      float4 x[kPairCtas];
-#pragma unroll
-      for (int r = 0; r < kPairCtas; ++r) {
-        mr[r] = *cluster.map_shared_rank(&cl_m[g], r);
-        lr[r] = *cluster.map_shared_rank(&cl_l[g], r);
-        x[r] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(smem + cl_at(g, e), r));
-      }
-      float mm = mr[0];
-#pragma unroll
-      for (int r = 1; r < kPairCtas; ++r) mm = fmaxf(mm, mr[r]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 oo = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 0; r < kPairCtas; ++r) {
-        if (mr[r] == -INFINITY) continue;  // its shared memory holds no result
-        const float f = exp2f(mr[r] - base);
-        ll = fmaf(lr[r], f, ll);
-        oo.x = fmaf(x[r].x, f, oo.x); oo.y = fmaf(x[r].y, f, oo.y);
-        oo.z = fmaf(x[r].z, f, oo.z); oo.w = fmaf(x[r].w, f, oo.w);
-      }
-      const int64_t h = (int64_t)cl_b * a.Hq + h0 + g;
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
-      const uint2 w = make_uint2(tc::pack_bf16(oo.x * inv, oo.y * inv), tc::pack_bf16(oo.z * inv, oo.w * inv));
-      *reinterpret_cast<uint2*>(a.out + h * C::kRowBytes + e * 2) = w;
-      if (e == 0 && a.lse) a.lse[h] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-    }
-    cluster.sync();  // no CTA leaves while another reads its shared memory
+  if constexpr (CL) join_cluster<__nv_bfloat16, D, H>(a, cl_b, cl_pair, share.u0 < u_end, part, part_at);
+}
+
+// ------------------------------------------------------------------ CUDA-core form (fp32)
+template <typename T, int N>
+struct LaneRow {
+  float v[N];
+};
+template <int N>
+__device__ __forceinline__ LaneRow<float, N> load_vec(const float* p) {
+  LaneRow<float, N> r;
+  if constexpr (N == 4) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    r.v[0] = x.x; r.v[1] = x.y; r.v[2] = x.z; r.v[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    r.v[0] = x.x; r.v[1] = x.y;
   }
+  return r;
+}
+
+// Each lane holds d / 32 elements of a row. U slots at a time, a warp forms the U GB
+// partial dot products and sums them over the lanes by halving: after step i a lane
+// keeps the half of the products its lane bit names, so the sums cost U GB - 1 exchanges
+// rather than 5 U GB, and the product of (slot u, head g) ends in the lanes whose top
+// bits are u GB + g. Softmax and mass scores are then one value per lane.
+// Bound: HBM while a kv head has few query heads (16 sequences of 2000 to 4000 slots, 8 kv
+// heads of 128, 4 query heads each: 68 us, 89% of the copy bandwidth); at 8 its issue slots
+// (8000 slots, 4 kv heads of 64: 66 us, 46%).
+template <typename C, int D, int GB, bool CL>
+__global__ void __launch_bounds__(kPagedThreads, C::kCtas)
+paged_fp32_kernel(const __grid_constant__ PagedArgs a) {
+  using Ring = typename C::Ring;
+  constexpr int N = D / 32, S = C::S, SLOTS = C::SLOTS;
+  constexpr int U = GB >= 8 ? 4 : 8;  // slots at a time
+  constexpr int P = U * GB;           // products: 8 .. 32
+  constexpr int SH = P == 32 ? 0 : P == 16 ? 1 : 2;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int warp_tmp[kPagedWarps];
+  __shared__ float s_m[kPagedWarps][8], s_l[kPagedWarps][8];
+  __shared__ __align__(16) float s_p[kPagedWarps][32];
+  __shared__ int64_t s_new[kPagedWarps * S];
+  __shared__ ClusterPart<CL ? 8 : 1> part;
+  int32_t* prefix = reinterpret_cast<int32_t*>(smem + C::kSmem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  Share share = plan_tiles<Ring::kTile>(a, prefix, warp_tmp);
+  write_empty_rows<float>(a, prefix, D);
+  [[maybe_unused]] int cl_b = 0, cl_pair = 0;
+  const auto part_at = [&](int g) { return reinterpret_cast<float*>(smem + Ring::kHalf) + g * D; };
+  if constexpr (CL) {
+    if (!cluster_share<Ring::kTile>(a, prefix, cl_b, cl_pair, share)) return;  // the whole cluster
+  } else if (share.u0 >= share.u1) {
+    return;
+  }
+  const int u_end = share.u1;
+  Ring ring(a, prefix, smem, s_new, share.u0, u_end);
+  Cursor<Ring::kTile> cc;
+  if (!CL || share.u0 < u_end) cc.seek(a, prefix, share.u0);
+  int stage = 0;
+  for (int u = share.u0; u < u_end;) {
+    const int b = cc.b, len = cc.len, tiles = cc.tiles, tile0 = cc.tile;
+    const int n_tiles = min(tiles - tile0, u_end - u);
+    const int kvh = cc.pair / a.blocks, blk = cc.pair - kvh * a.blocks;
+    const Piece piece{b, kvh * a.G + blk * a.heads, min(a.heads, a.G - blk * a.heads), tile0 == 0,
+                      n_tiles == tiles};
+    const int new_tile = a.k_new && blk == 0 && ((len - 1) % Ring::kTile) / SLOTS == warp ? tiles - 1 - tile0 : -1;
+    const int new_row = (len - 1) % SLOTS;
+    float q[GB][N];
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+      const auto x = load_vec<N>(reinterpret_cast<const float*>(a.q + (int64_t)b * a.q_bytes) +
+                                 (int64_t)(piece.h0 + min(g, piece.heads - 1)) * D + lane * N);
+#pragma unroll
+      for (int e = 0; e < N; ++e) q[g][e] = x.v[e] * a.scale2;
+    }
+    float m = -INFINITY, l = 0.f;  // of head (lane >> SH) % GB
+    float o[GB][N];
+#pragma unroll
+    for (int g = 0; g < GB; ++g)
+#pragma unroll
+      for (int e = 0; e < N; ++e) o[g][e] = 0.f;
+    for (int i = 0; i < n_tiles; ++i) {
+      __syncwarp();  // every lane has read the stage that is filled next
+      ring.issue(stage == 0 ? S - 1 : stage - 1);
+      const uint32_t held = ring.held(stage);
+      const uint8_t* kb = smem + (warp * S + stage) * Ring::kStage;
+      const auto row = [&](const uint8_t* base, int r) {  // this lane's elements of a staged row
+        return load_vec<N>(reinterpret_cast<const float*>(base + Ring::chunk(r, lane * N / 4)) + lane * N % 4);
+      };
+      cp_async_wait<2 * S - 2>();
+      __syncwarp();
+#pragma unroll 1
+      for (int r0 = 0; r0 < SLOTS; r0 += U) {
+        float s[P];
+#pragma unroll
+        for (int i2 = 0; i2 < U; ++i2) {
+          const auto k = row(kb, r0 + i2);
+#pragma unroll
+          for (int g = 0; g < GB; ++g) {
+            float t = 0.f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) t = fmaf(q[g][e], k.v[e], t);
+            s[i2 * GB + g] = t;
+          }
+        }
+        int n = P;
+#pragma unroll
+        for (int bit = 16; bit > 0; bit >>= 1) {
+          if (n > 1) {
+            n >>= 1;
+            const bool up = lane & bit;
+#pragma unroll
+            for (int i2 = 0; i2 < P / 2; ++i2)
+              if (i2 < n) {
+                const float mine = up ? s[i2 + n] : s[i2], give = up ? s[i2] : s[i2 + n];
+                s[i2] = mine + __shfl_xor_sync(0xffffffffu, give, bit);
+              }
+          } else {
+            s[0] += __shfl_xor_sync(0xffffffffu, s[0], bit);
+          }
+        }
+        const int c = lane >> SH, iu = c / GB, ig = c % GB;
+        const float sc = (held >> (r0 + iu)) & 1u ? s[0] : -INFINITY;
+        if (a.scores && (lane & ((1 << SH) - 1)) == 0) {
+          const int j = (tile0 + i) * Ring::kTile + warp * SLOTS + r0 + iu;
+          if (ig < piece.heads && j < len) a.scores[((int64_t)b * a.Hq + piece.h0 + ig) * a.score_row + j] = sc;
+        }
+        float mx = sc;
+#pragma unroll
+        for (int bit = 16; bit >= 32 / U; bit >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, bit));
+        const float mn = fmaxf(m, mx);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float p = exp2f(sc - base), alpha = exp2f(m - base);
+        float ps = p;
+#pragma unroll
+        for (int bit = 16; bit >= 32 / U; bit >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, bit);
+        l = l * alpha + ps;
+        m = mn;
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+          const float al = __shfl_sync(0xffffffffu, alpha, g << SH);
+#pragma unroll
+          for (int e = 0; e < N; ++e) o[g][e] *= al;
+        }
+        if constexpr (GB >= 4) {  // a slot's weights of four heads in one broadcast read
+          __syncwarp();
+          s_p[warp][lane] = p;  // P = 32: the lane is the product
+          __syncwarp();
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < U; ++i2) {
+          const auto v = row(kb + Ring::kHalf, r0 + i2);
+          float w[GB];
+          if constexpr (GB >= 4) {
+#pragma unroll
+            for (int g = 0; g < GB; g += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(&s_p[warp][i2 * GB + g]);
+              w[g] = x.x; w[g + 1] = x.y; w[g + 2] = x.z; w[g + 3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < GB; ++g) w[g] = __shfl_sync(0xffffffffu, p, (i2 * GB + g) << SH);
+          }
+#pragma unroll
+          for (int g = 0; g < GB; ++g)
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[g][e] = fmaf(w[g], v.v[e], o[g][e]);
+        }
+      }
+      if (i == new_tile && ((held >> new_row) & 1u)) ring.keep_new(stage, new_row);
+      stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    const int last = stage == 0 ? S - 1 : stage - 1;
+    const auto joined = [&](int w) { return reinterpret_cast<float*>(smem + (w * S + last) * Ring::kStage); };
+    __syncwarp();
+    if (lane < (GB << SH) && (lane & ((1 << SH) - 1)) == 0) {
+      s_m[warp][lane >> SH] = m;
+      s_l[warp][lane >> SH] = l;
+    }
+#pragma unroll
+    for (int g = 0; g < GB; ++g)
+#pragma unroll
+      for (int e = 0; e < N; ++e) joined(warp)[g * D + ((lane * N + e) ^ (((g >> 1) & 3) << 3))] = o[g][e];
+    __syncthreads();
+    join_warps<float, D, 8, CL>(a, piece, 0, s_m, s_l, joined, part, part_at(0));
+    u += n_tiles;
+    if (!CL && u < u_end) {
+      __syncthreads();  // every warp has read the results: the stage is free
+      cc.tile = tile0 + n_tiles - 1;
+      cc.next(a, prefix, u);
+    }
+  }
+  if constexpr (CL) join_cluster<float, D, 8>(a, cl_b, cl_pair, share.u0 < u_end, part, part_at);
 }
 
 // ------------------------------------------------------------------ join and masses
@@ -1005,22 +1046,6 @@ PagedWorkspace paged_layout(int B, int Hq, int d, int max_len, bool mass, int he
 }
 
 int64_t sequence_heads(const PagedArgs& a) { return (int64_t)a.B * a.c.Hkv * a.blocks; }
-int paged_grid(int64_t tiles, int per_sm) {
-  int64_t most = (int64_t)device_info().sm_count * per_sm;
-  if (most > kMaxPagedGrid) most = kMaxPagedGrid;
-  return (int)(tiles < most ? tiles : most);
-}
-
-template <typename T, int D>
-cudaError_t launch_simt(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
-  a.grid = paged_grid(tiles, 4);
-  switch (a.heads) {
-    case 1: return launch_dependent(paged_simt_kernel<T, D, 1>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
-    case 2: return launch_dependent(paged_simt_kernel<T, D, 2>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
-    case 3: case 4: return launch_dependent(paged_simt_kernel<T, D, 4>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
-    default: return launch_dependent(paged_simt_kernel<T, D, 8>, dim3(a.grid), dim3(kPagedThreads), smem, stream, a);
-  }
-}
 
 // bf16: up to 16 heads in one pass over the cache (two column tiles); fp32: 8.
 int heads_per_block(int G, bool bf16) {
@@ -1028,27 +1053,25 @@ int heads_per_block(int G, bool bf16) {
   return (G + blocks - 1) / blocks;
 }
 
-template <int D, int NT, int S, bool CL = false>
-cudaError_t launch_mma(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
-  using C = MmaCfg<D, NT, S>;
-  static thread_local int configured_for = -1;
+template <typename C, bool CL>
+cudaError_t launch_split(void (*kernel)(PagedArgs), int& configured_for, PagedArgs& a, cudaStream_t stream) {
   const DeviceInfo& dev = device_info();
-  const auto kernel = paged_mma_kernel<D, NT, S, CL>;
   if (configured_for != dev.device) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                C::kSmem + (kPagedMaxBatch + 1) * 4);
     if (e != cudaSuccess) return e;
     configured_for = dev.device;
   }
-  if (!CL) {
-    a.grid = paged_grid(tiles, C::kCtas);
-    return launch_dependent(kernel, dim3(a.grid), dim3(kPagedThreads), C::kSmem + smem, stream, a);
-  }
-  a.grid = (int)sequence_heads(a) * kPairCtas;
+  a.even_pages = a.c.page.n % C::SLOTS == 0;
+  const int64_t pairs = sequence_heads(a);
+  int64_t ctas = a.split == PagedSplit::kWhole ? pairs : pairs * tile_count(a.max_len, C::Ring::kTile);
+  const int64_t most = std::min<int64_t>((int64_t)dev.sm_count * C::kCtas, kMaxPagedGrid);
+  ctas = CL ? pairs * kPairCtas : std::min(ctas, most);
+  a.grid = (int)ctas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.grid);
   cfg.blockDim = dim3(kPagedThreads);
-  cfg.dynamicSmemBytes = C::kSmem + smem;
+  cfg.dynamicSmemBytes = C::kSmem + ((size_t)a.B + 1) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1057,18 +1080,47 @@ cudaError_t launch_mma(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t st
   attr[1].val.clusterDim.x = kPairCtas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = CL ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
+template <typename C, int D, int NT, bool CL = false>
+cudaError_t launch_mma(PagedArgs& a, cudaStream_t stream) {
+  static thread_local int configured_for = -1;
+  return launch_split<C, CL>(paged_mma_kernel<C, D, NT, CL>, configured_for, a, stream);
+}
+template <typename C, int D, int GB, bool CL>
+cudaError_t launch_fp32_heads(PagedArgs& a, cudaStream_t stream) {
+  static thread_local int configured_for = -1;
+  return launch_split<C, CL>(paged_fp32_kernel<C, D, GB, CL>, configured_for, a, stream);
+}
 
+// Stages of a warp's ring. Two CTAs an SM with three stages keep the most bytes in flight,
+// which one long sequence wants (bf16, 131071 slots, 8 kv heads: 88.7 us, against 92.9 with
+// three CTAs of two stages). Where there are as many sequence-heads as SMs their ends and
+// starts cost more, and a third CTA works through them (7 sequences of 32 kv heads: 26.9 us
+// against 29.0; 64 of 4: 109.5 against 111.0).
 template <int D>
-cudaError_t launch_bf16(PagedArgs& a, int64_t tiles, size_t smem, cudaStream_t stream) {
+cudaError_t launch_bf16(PagedArgs& a, cudaStream_t stream) {
+  using T = __nv_bfloat16;
+  using Deep = PagedCfg<T, D, 3, 2>;
+  using Wide = PagedCfg<T, D, 2, 3>;
+  using Heads16 = PagedCfg<T, D, D == 128 ? 2 : 3, 2>;  // registers: two CTAs
   if (a.split == PagedSplit::kCluster)
-    return a.heads > 8 ? launch_mma<D, 2, D == 128 ? 2 : 3, true>(a, tiles, smem, stream)
-                       : launch_mma<D, 1, 3, true>(a, tiles, smem, stream);
-  if (a.heads > 8) return launch_mma<D, 2, D == 128 ? 2 : 3>(a, tiles, smem, stream);
-  if (sequence_heads(a) >= device_info().sm_count) return launch_mma<D, 1, 2>(a, tiles, smem, stream);
-  return launch_mma<D, 1, 3>(a, tiles, smem, stream);
+    return a.heads > 8 ? launch_mma<Heads16, D, 2, true>(a, stream) : launch_mma<Deep, D, 1, true>(a, stream);
+  if (a.heads > 8) return launch_mma<Heads16, D, 2>(a, stream);
+  return sequence_heads(a) >= device_info().sm_count ? launch_mma<Wide, D, 1>(a, stream)
+                                                     : launch_mma<Deep, D, 1>(a, stream);
+}
+
+template <int D, bool CL>
+cudaError_t launch_fp32(PagedArgs& a, cudaStream_t stream) {
+  using C = PagedCfg<float, D, 3, 2>;
+  switch (a.heads) {
+    case 1: return launch_fp32_heads<C, D, 1, CL>(a, stream);
+    case 2: return launch_fp32_heads<C, D, 2, CL>(a, stream);
+    case 3: case 4: return launch_fp32_heads<C, D, 4, CL>(a, stream);
+    default: return launch_fp32_heads<C, D, 8, CL>(a, stream);
+  }
 }
 
 }  // namespace
@@ -1102,7 +1154,7 @@ size_t paged_attention_workspace(int B, int Hq, int Hkv, int d, int max_len, boo
 }
 
 int64_t paged_attention_tiles(int B, int Hq, int max_len) {
-  return (int64_t)B * Hq * ((max_len + kTile - 1) / kTile);
+  return (int64_t)B * Hq * tile_count(max_len, 32);  // the smaller tile
 }
 
 cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
@@ -1120,7 +1172,6 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.heads = heads_per_block(a.G, c.dtype == DD_BF16);
   a.blocks = (a.G + a.heads - 1) / a.heads;
   a.max_len = p.max_len;
-  a.even_pages = c.page_size % kWarpSlots == 0;
   a.scale2 = (p.scale > 0.f ? p.scale : 1.f / sqrtf((float)c.d)) * kLog2e;
   a.out = static_cast<char*>(p.out);
   a.lse = p.lse;
@@ -1133,8 +1184,6 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   a.score_row = score_row(p.max_len);
   a.scores = p.mass_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
-  const int64_t tiles = (int64_t)p.B * c.Hkv * a.blocks * ((p.max_len + kTile - 1) / kTile);
-  const size_t smem = ((size_t)p.B + 1) * 4;
   // Short sequences take one launch, with nothing left to a join. With as many sequence-heads
   // as SMs whole ones fill the GPU (64 sequences of 4 kv heads, 512 slots: 15.1 us, 19.5 split;
   // 8 kv heads, 256 slots: 16.9, 18.5); with few, a CTA would walk through its tiles alone (one
@@ -1145,15 +1194,16 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.split = PagedSplit::kRanges;
   if (!p.mass_out && p.max_len <= kWholeLen) {
     const int64_t pairs = sequence_heads(a);
-    if (pairs >= device_info().sm_count || p.max_len <= kTile) a.split = PagedSplit::kWhole;
-    else if (c.dtype == DD_BF16 && pairs * kPairCtas <= 2 * device_info().sm_count) a.split = PagedSplit::kCluster;
+    if (pairs >= device_info().sm_count || p.max_len <= kTileSlots) a.split = PagedSplit::kWhole;
+    else if (pairs * kPairCtas <= 2 * device_info().sm_count) a.split = PagedSplit::kCluster;
   }
-  const int64_t units = a.split == PagedSplit::kWhole ? sequence_heads(a) : tiles;
   cudaError_t err;
   if (c.dtype == DD_BF16)
-    err = c.d == 128 ? launch_bf16<128>(a, units, smem, stream) : launch_bf16<64>(a, units, smem, stream);
+    err = c.d == 128 ? launch_bf16<128>(a, stream) : launch_bf16<64>(a, stream);
+  else if (a.split == PagedSplit::kCluster)
+    err = c.d == 128 ? launch_fp32<128, true>(a, stream) : launch_fp32<64, true>(a, stream);
   else
-    err = c.d == 128 ? launch_simt<float, 128>(a, units, smem, stream) : launch_simt<float, 64>(a, units, smem, stream);
+    err = c.d == 128 ? launch_fp32<128, false>(a, stream) : launch_fp32<64, false>(a, stream);
   if (err != cudaSuccess || a.split != PagedSplit::kRanges) return err;
   // join: a CTA per query head; masses: enough CTAs a sequence to fill the GPU a few times
   int mass_ctas = 0;
