@@ -370,7 +370,7 @@ dd_status dd_select_seeds_ex(
  * only read. A page id below 0 is a hole: its slots are not read and take no part in
  * the softmax. A page id of n_pages or more, or a length outside [0, max_len], is an
  * error found on the device: it records DD_ERR_BOUNDS, the page counts as a hole, the
- * length is clamped.
+ * length is clamped (and nothing is appended to such a sequence).
  * Strides are in elements and whole multiples of 16 bytes; k and v are 16-byte
  * aligned. page_size is any number from 1 on. */
 typedef struct {
@@ -476,16 +476,17 @@ dd_status dd_cache_evict(
  * dd_beam_select -- one step of beam search over B requests of K beams:
  *   score(k, v) = score_in[k] + x_kv - log sum_u e^{x_ku}   for every token of a live beam,
  *   a beam that is done (done_in) has the one candidate (k, eos) at its own score,
- *   a beam whose score_in is -inf or NaN has none (an empty slot).
- * The K best of the K V candidates, by score, equal scores by the lower k V + v; scores
- * are compared in 64 bits. A logit of -inf (or NaN) is no candidate and adds nothing to
- * the sum; +inf is not allowed. Where there are fewer than K candidates the rest get
+ *   a beam whose score_in is not finite has none (an empty slot: -inf).
+ * The K best of the K V candidates, by score; equal scores: the lower beam, then the larger
+ * logit, then the lower token. Scores are compared in 64 bits (the sum's error, about 1e-7, is what can order two beams'
+ * candidates wrongly). A logit that is not finite (-inf: a banned token) is no candidate and
+ * adds nothing to the sum. Where there are fewer than K candidates the rest get
  * parent -1, token -1, score -inf, done 0.
  *
  * logits          [B,K,V], row stride ld >= V, DD_F32 or DD_BF16, 16-byte aligned,
  *                 ld * element a multiple of 16 bytes
  * score_in        [B,K] fp32; done_in [B,K] u8 or NULL (none); eos in [-1, V), -1: no token
- *                 ends a beam (a done beam then stands at k V and gets token -1)
+ *                 ends a beam (a done beam then gets token -1)
  * parent, token   [B,K] int32; score_out [B,K] fp32 in descending order (not score_in's memory);
  * done_out        [B,K] u8 or NULL: the parent was done, or the token is eos (not done_in's
  *                 memory)
@@ -516,7 +517,7 @@ typedef struct {
 /*
  * dd_beam_reorder -- states follow their parents: row b K + k of each dst is row
  * b K + parent[b,k] of its src. A parent outside [0, K) (an empty slot) keeps its own
- * row k. Up to 8 states in one launch; src and dst of a state must not overlap.
+ * row k. Up to 8 states in one launch; no dst may overlap any src or other dst.
  * Errors: DD_ERR_INVALID_ARG for null pointers, sizes, strides below row_bytes (either
  * may be anything when B * K = 1), src == dst; DD_ERR_UNSUPPORTED for n_states > 8 or
  * B * K > 2^20.

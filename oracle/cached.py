@@ -79,28 +79,33 @@ def evict_one(mass, pos, budget, sink, recent):
 
 
 def beam_candidates(logits, score, done, eos, V, most):
-    """(minus score, flat index) of the first `most` candidates of one request, best first."""
-    values, places = [], []
+    """(minus score, flat index) of the first `most` candidates of one request, best first;
+    equal scores: the lower beam, the larger logit, the lower token."""
+    values, places, beams, logit = [], [], [], []
     for k in range(len(score)):
         base = float(score[k])
-        if not base > -np.inf:
+        if not np.isfinite(base):
             continue
         if done is not None and done[k]:
             values.append(np.array([base]))
             places.append(np.array([k * V + max(eos, 0)]))
+            beams.append(np.array([k]))
+            logit.append(np.zeros(1))
             continue
         x = np.array(logits[k], dtype=np.float64)
-        live = x > -np.inf  # False for NaN
+        live = np.isfinite(x)
         if not live.any():
             continue
         m = x[live].max()
         lse = m + np.log(np.exp(x[live] - m).sum())
         values.append(base + (x[live] - lse))
         places.append(k * V + np.nonzero(live)[0])
+        beams.append(np.full(int(live.sum()), k))
+        logit.append(x[live])
     if not values:
         return []
-    values, places = np.concatenate(values), np.concatenate(places)
-    order = np.lexsort((places, -values))[:most]
+    values, places, beams, logit = (np.concatenate(a) for a in (values, places, beams, logit))
+    order = np.lexsort((places, -logit, beams, -values))[:most]
     return [(-float(values[i]), int(places[i])) for i in order]
 
 

@@ -32,8 +32,8 @@ __device__ __forceinline__ uint32_t logit_key(float x) {
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
-// NaN is no candidate; -0 ties with 0.
-__device__ __forceinline__ float clean_logit(float x) { return x == x ? x + 0.f : -INFINITY; }
+// NaN and +inf are no candidates; -0 ties with 0.
+__device__ __forceinline__ float clean_logit(float x) { return x < INFINITY ? x + 0.f : -INFINITY; }
 
 // The two (bf16) or one (fp32) logits of a 32-bit word.
 template <typename T>
@@ -66,7 +66,7 @@ __device__ __forceinline__ float max_of(uint32_t w, float) { return __uint_as_fl
 __device__ __forceinline__ bool scans(const float* score_in, const uint8_t* done_in, int row) {
   const float s = score_in[row];
   const uint8_t d = done_in ? done_in[row] : 0;  // both loads in flight at once
-  return s > -INFINITY && !d;
+  return isfinite(s) && !d;
 }
 
 // The largest 16-bit p that at least `want` of the block's keys reach, bit by bit; all threads
@@ -134,7 +134,18 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     mw[2] = max_word(mw[2], v.z, T{});
     mw[3] = max_word(mw[3], v.w, T{});
   }
-  const float mx = max_of(max_word(max_word(mw[0], mw[1], T{}), max_word(mw[2], mw[3], T{}), T{}), T{}) + 0.f;
+  float mx = max_of(max_word(max_word(mw[0], mw[1], T{}), max_word(mw[2], mw[3], T{}), T{}), T{}) + 0.f;
+  if (mx == INFINITY) {  // not a candidate: again, without such logits
+    mx = -INFINITY;
+    for (int i = 0; i < kBeamVecs; ++i) {
+      const uint4 v = seg[i * kBeamThreads];
+      const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int h = 0; h < W::n; ++h) mx = fmaxf(mx, clean_logit(W::get(r[e], h)));
+    }
+  }
   const uint32_t mine = logit_key(mx) >> 16;
   const uint32_t bound = kth_key16(mine, K);
   // sum of exponentials relative to the segment's maximum
@@ -153,7 +164,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
         for (int h = 0; h < W::n; ++h) part[e] += fast_exp2(fmaf(W::get(r[e], h), kLog2e, -ref));
     }
     sum = (part[0] + part[1]) + (part[2] + part[3]);
-    if (sum != sum) {  // NaN logits add nothing
+    if (!(sum < INFINITY)) {  // NaN and +inf logits add nothing
       sum = 0.f;
       for (int i = 0; i < kBeamVecs; ++i) {
         const uint4 v = seg[i * kBeamThreads];
@@ -279,9 +290,18 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   }
 }
 
+// A candidate's place among those of equal score, smaller first: the beam, then the larger
+// logit (which a 64-bit score far from zero no longer tells apart), then the token.
+__device__ __forceinline__ int64_t place_of(int k, uint32_t key, int v) {
+  return ((int64_t)k << 55) | ((int64_t)(0xFFFFFFFFu - key) << 23) | v;
+}
+__device__ __forceinline__ int place_beam(int64_t at) { return (int)(at >> 55); }
+__device__ __forceinline__ int place_token(int64_t at) { return (int)(at & ((1 << 23) - 1)); }
+static_assert(kBeamMaxV <= 1 << 23 && kBeamMaxK <= 1 << 7);
+
 struct Best {
   double score;
-  int64_t at;  // k V + v
+  int64_t at;
   int list;
 };
 __device__ __forceinline__ bool better(double s, int64_t at, double s2, int64_t at2) {
@@ -300,10 +320,10 @@ struct BeamOut {
   uint8_t* done;
   int eos;
 };
-// Rank r of request b: candidate `at` = k V + v of beam k (k < 0: none).
+// Rank r of a request: token v of beam k (k < 0: none).
 __device__ __forceinline__ void write_beam(const BeamOut& o, int64_t r, int k, bool was_done, double score,
-                                           int64_t at, int V) {
-  const int v = k < 0 ? -1 : was_done ? o.eos : (int)(at - (int64_t)k * V);
+                                           int token) {
+  const int v = k < 0 ? -1 : was_done ? o.eos : token;
   o.parent[r] = k < 0 ? -1 : k;
   o.token[r] = v;
   o.score[r] = k < 0 ? -INFINITY : (float)score;
@@ -316,7 +336,7 @@ __device__ __forceinline__ void write_beam(const BeamOut& o, int64_t r, int k, b
 // distances below the best score by their top 16 bits: 1 part in 128, whatever the scores'
 // size.) Should more than kBeamList reach it, K rounds over the lists' heads pick one each.
 __global__ void __launch_bounds__(kBeamThreads)
-beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
+beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
                   const uint8_t* __restrict__ done_in, const float2* __restrict__ ml,
                   const uint2* __restrict__ cand, BeamOut res) {
   pdl_wait();
@@ -344,7 +364,7 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
   if (threadIdx.x < K) {
     const float s = score_in[b * K + threadIdx.x];
     const bool done = done_in && done_in[b * K + threadIdx.x];
-    s_kind[threadIdx.x] = !(s > -INFINITY) ? 0 : done ? 2 : 1;
+    s_kind[threadIdx.x] = !isfinite(s) ? 0 : done ? 2 : 1;
     s_base[threadIdx.x] = (double)s;
   }
   if (threadIdx.x == 0) s_n = 0;
@@ -377,13 +397,13 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
   const auto entry = [&](int k, const uint2& c, double& s, int64_t& at) {
     if (s_kind[k] != 1 || c.x <= kNone) return false;
     s = s_base[k] + (double)key_logit(c.x);
-    at = (int64_t)k * V + c.y;
+    at = place_of(k, c.x, (int)c.y);
     return true;
   };
   const auto ended = [&](int k, double& s, int64_t& at) {
     if (s_kind[k] != 2) return false;
     s = s_base[k];
-    at = (int64_t)k * V + (res.eos > 0 ? res.eos : 0);
+    at = place_of(k, 0u, 0);
     return true;
   };
   // this thread's candidates: warp w has beams w, w + 8, ..., a lane every 32nd entry
@@ -429,11 +449,11 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
       const int64_t at = s_at[i];
       int r = 0;
       for (int t = 0; t < n; ++t) r += better(s_score[t], s_at[t], s, at);
-      const int k = (int)(at / V);
-      if (r < K) write_beam(res, (int64_t)b * K + r, k, s_kind[k] == 2, s, at, V);
+      const int k = place_beam(at);
+      if (r < K) write_beam(res, (int64_t)b * K + r, k, s_kind[k] == 2, s, place_token(at));
     }
     for (int r = n + threadIdx.x; r < K; r += kBeamThreads)
-      write_beam(res, (int64_t)b * K + r, -1, false, 0.0, 0, V);
+      write_beam(res, (int64_t)b * K + r, -1, false, 0.0, 0);
     return;
   }
   // ---- K rounds: the best head of the sorted lists, whose list steps on
@@ -468,7 +488,7 @@ beam_merge_kernel(int K, int V, int pieces, const float* __restrict__ score_in,
     __syncthreads();
     if (threadIdx.x == 0) {
       const int k = x.list >= 0 ? x.list / pieces : -1;
-      write_beam(res, (int64_t)b * K + r, k, k >= 0 && s_kind[k] == 2, x.score, x.at, V);
+      write_beam(res, (int64_t)b * K + r, k, k >= 0 && s_kind[k] == 2, x.score, place_token(x.at));
     }
     if (x.list >= 0 && x.list % kBeamThreads == (int)threadIdx.x) {
       head[x.list] += 1;
@@ -513,8 +533,8 @@ cudaError_t launch_beam_select(const BeamCall& p, cudaStream_t stream) {
     configured_for = device_info().device;
   }
   const BeamOut res{p.parent, p.token, p.score_out, p.done_out, p.eos};
-  return launch_dependent(beam_merge_kernel, dim3(p.B), dim3(kBeamThreads), (size_t)p.K * pieces, stream, p.K,
-                          p.V, pieces, p.score_in, p.done_in, (const float2*)ml, (const uint2*)cand, res);
+  return launch_dependent(beam_merge_kernel, dim3(p.B), dim3(kBeamThreads), (size_t)p.K * pieces, stream, p.K, pieces,
+                          p.score_in, p.done_in, (const float2*)ml, (const uint2*)cand, res);
 }
 
 }  // namespace dd

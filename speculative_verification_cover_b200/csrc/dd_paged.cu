@@ -145,14 +145,21 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
+// The slot of a sequence's new token: its last, or -1 without one (or with a length out of
+// range, which is clamped to read by but not to write by).
+__device__ __forceinline__ int new_slot(const PagedArgs& a, int b, int len) {
+  return a.k_new && a.lengths[b] == len ? len - 1 : -1;
+}
+
 // A place in the tile space: tile `tile` of (sequence b, pair = kv head and head block).
 template <int TILE>
 struct Cursor {
-  int b, len, tiles, pair, tile;
+  int b, len, tiles, fresh, pair, tile;  // fresh: the new token's slot
   __device__ __forceinline__ void enter(const PagedArgs& a, int at) {
     b = at;
     len = checked_length(a.lengths, b, a.max_len);
     tiles = tile_count(len, TILE);
+    fresh = new_slot(a, b, len);
   }
   __device__ __forceinline__ void seek(const PagedArgs& a, const int32_t* prefix, int u) {
     enter(a, find_sequence(prefix, a.B, u));
@@ -241,7 +248,7 @@ struct SlotRing {
       off = (int64_t)page * a.c.page_bytes + (int64_t)kvh * a.c.head_bytes +
             (int64_t)(j - div_fast(a.c.page, j) * a.c.page.n) * a.c.token_bytes;
     const uint32_t rows = __ballot_sync(0xffffffffu, ok) & kAll;
-    const uint32_t fresh = __ballot_sync(0xffffffffu, ok && a.k_new && j == lc.len - 1) & kAll;
+    const uint32_t fresh = __ballot_sync(0xffffffffu, ok && j == lc.fresh) & kAll;
     held_q = (held_q & ~((uint64_t)kAll << (SLOTS * stage))) | ((uint64_t)rows << (SLOTS * stage));
     if ((fresh >> (lane % SLOTS)) & 1u) new_at[stage] = off;  // the slot's lanes: the same
     const uint32_t dst = k_at(stage);
@@ -496,8 +503,8 @@ paged_mma_kernel(const __grid_constant__ PagedArgs a) {
     const int h0 = piece.h0, nh = piece.heads;
     // the tile of this piece, if any, whose slots of this warp hold the new token
     const int new_tile =
-        a.k_new && blk == 0 && ((len - 1) % Ring::kTile) / C::SLOTS == warp ? tiles - 1 - tile0 : -1;
-    const int new_row = (len - 1) % C::SLOTS;
+        cc.fresh >= 0 && blk == 0 && cc.fresh % Ring::kTile / C::SLOTS == warp ? tiles - 1 - tile0 : -1;
+    const int new_row = cc.fresh % C::SLOTS;
     uint32_t q[NT][KS][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -707,8 +714,9 @@ paged_fp32_kernel(const __grid_constant__ PagedArgs a) {
     const int kvh = cc.pair / a.blocks, blk = cc.pair - kvh * a.blocks;
     const Piece piece{b, kvh * a.G + blk * a.heads, min(a.heads, a.G - blk * a.heads), tile0 == 0,
                       n_tiles == tiles};
-    const int new_tile = a.k_new && blk == 0 && ((len - 1) % Ring::kTile) / SLOTS == warp ? tiles - 1 - tile0 : -1;
-    const int new_row = (len - 1) % SLOTS;
+    const int new_tile =
+        cc.fresh >= 0 && blk == 0 && cc.fresh % Ring::kTile / SLOTS == warp ? tiles - 1 - tile0 : -1;
+    const int new_row = cc.fresh % SLOTS;
     float q[GB][N];
 #pragma unroll
     for (int g = 0; g < GB; ++g) {
@@ -989,6 +997,7 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
   }
   __syncwarp();
   const float inv = 1.f / (float)a.Hq;
+  const int fresh = new_slot(a, b, len);
   for (int first = part * kMassChunk; first < len; first += kMassChunk * mass_ctas) {
     j = first + 4 * lane;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1011,8 +1020,7 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) total += reinterpret_cast<const float*>(s_sum[w])[threadIdx.x];
       const int64_t o = (int64_t)b * a.mass_stride + at;
-      const bool fresh = a.k_new && at == len - 1;
-      const float before = a.mass_in && !fresh ? a.mass_in[o] : 0.f;
+      const float before = a.mass_in && at != fresh ? a.mass_in[o] : 0.f;
       a.mass_out[o] = before + total * inv;
     }
     __syncthreads();

@@ -373,9 +373,10 @@ def _gpu(t, name):
     """Index of the device a call runs on: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
+    gpu = t.get_device()
+    if gpu < 0:
         raise ValueError(f"libdd takes device memory: {name} is on the CPU")
-    return t.get_device()
+    return gpu
 
 
 def _refuse(t, name, dtype, shape, gpu, rows):
@@ -433,17 +434,17 @@ def _workspace(t, gpu):
 
 def _call(name, gpu, stream, *args):
     """A library call on device `gpu` (made current only where it is not), on `stream`."""
-    fn = getattr(lib(), name)
+    fn = getattr(_lib or lib(), name)
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(gpu)
     else:
         s = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == gpu:
+    if torch._C._cuda_getDevice() == gpu:
         st = fn(*args, s)
     else:
         with torch.cuda.device(gpu):
             st = fn(*args, s)
-    if st != DD_OK:
+    if st:
         raise DDError(name, st)
 
 

@@ -210,3 +210,70 @@ def test_fork_records_bad_pages_and_lengths():
     dd.dd_paged_fork(cache, t([[0, 1]]), t([100, -3]), t([4, 5]), out, lout)
     assert dd.dd_get_device_error() == dd.DD_ERR_BOUNDS
     assert torch.equal(k, k0) and out.tolist() == [[0, 1], [5, -1]] and lout.tolist() == [8, 0]
+
+
+def test_more_pieces_and_entries_than_are_held_on_chip():
+    x, score = _logits(20, 1, 64, 152064, torch.bfloat16)
+    _check(x, score)
+    x, score = _logits(21, 1, 48, 152064, torch.float32)
+    _check(x, score)
+    _check(torch.zeros_like(x), torch.zeros_like(score), gaps=False)
+
+
+def test_values_that_are_not_finite():
+    inf, nan = float("inf"), float("nan")
+    for dtype in (torch.bfloat16, torch.float32):
+        x, score = _logits(22, 2, 4, 20000, dtype)
+        x[0, 0, 7] = inf                   # no candidate, not in the sum
+        x[0, 1, ::3] = nan
+        x[0, 2, :] = inf
+        x[1, 3, 16384:] = -inf
+        x[1, 2, 100:9000] = inf
+        score[1, 0] = inf                  # empty slots
+        score[1, 1] = nan
+        got = _check(x, score)
+        assert 0 not in got[0][1] and 1 not in got[0][1] and 2 not in got[0][0]
+
+
+def test_scores_of_any_size():
+    # far below zero (a long hypothesis), and far apart
+    x, score = _logits(23, 2, 8, 5000, torch.bfloat16)
+    wide = score * 1e4
+    _check(x, wide)
+    _check(x, score * 1e30, gaps=False)
+
+
+def test_refusals_of_the_binding():
+    x, score = _logits(24, 2, 4, 1000, torch.bfloat16)
+    i = dict(dtype=torch.int32, device="cuda")
+
+    def call(**over):
+        a = dict(logits=x, score=score, parent=torch.zeros(2, 4, **i), token=torch.zeros(2, 4, **i),
+                 score_out=torch.zeros(2, 4, device="cuda"))
+        a.update(over)
+        dd.dd_beam_select(**a)
+
+    call()
+    for over in (dict(logits=x.half()), dict(logits=x.cpu()), dict(logits=x[:, :3]), dict(logits=x[..., ::2]), dict(logits=x[0]),
+                 dict(logits=x.transpose(0, 1)), dict(score=score.double()), dict(score=score[:1]), dict(parent=torch.zeros(2, 4)),
+                 dict(done=torch.zeros(2, 4, dtype=torch.bool, device="cuda")), dict(token=torch.zeros(2, 4, dtype=torch.int32)),
+                 dict(workspace=torch.zeros(10))):
+        with pytest.raises((ValueError, TypeError)):
+            call(**over)
+    for over in (dict(score_out=score), dict(eos=1000), dict(eos=-2), dict(logits=x[..., :999], eos=999),
+                 dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(dd.DDError):
+            call(**over)
+    parent = torch.zeros(2, 4, **i)
+    s = torch.zeros(8, 5, device="cuda")
+    for pair in ((s, s), (s, s[:, :4]), (s, s.int()), (s.cpu(), s), (torch.zeros(16, 5, device="cuda")[:8], torch.zeros(7, 5, device="cuda")),
+                 (s.t().contiguous().t(), s.clone())):
+        with pytest.raises((ValueError, TypeError)):
+            dd.dd_beam_reorder(parent, [pair])
+    big = torch.zeros(12, 5, device="cuda")
+    with pytest.raises(ValueError):                     # one within the other's memory
+        dd.dd_beam_reorder(parent, [(big[:8], big[4:])])
+    with pytest.raises(dd.DDError):
+        dd.dd_beam_reorder(parent, [])
+    with pytest.raises(dd.DDError):
+        dd.dd_beam_reorder(parent, [(s, s.clone())] * 9)

@@ -144,3 +144,63 @@ def test_holes_and_bad_values_move_nothing():
     n.fill_(-1)
     dd.dd_cache_evict(dd.PagedCache(k, v, table.cuda()), n, mass, pos, 8, *out, no)
     assert int(no) == 0 and dd.dd_get_device_error() == dd.DD_ERR_BOUNDS
+
+
+@pytest.mark.parametrize("length,budget", [(290001, 100), (400000, 399000), (524288, 262144)])
+def test_longest(length, budget):
+    # keys that do not fit shared memory; the most movers there can be
+    _run(20, budget, 3, 10, N=1, page=64, Hkv=1, d=64, lengths=[length])
+    _run(21, budget, 0, 0, N=1, page=64, Hkv=1, d=64, lengths=[length], ties=True)
+
+
+@pytest.mark.parametrize("lengths", [[2048, 2049, 100], [2049], [9000, 0, 1, 3000]])
+def test_around_the_cluster_s_length(lengths):
+    for budget in (1, 100, 2000, 2048):
+        _run(22, budget, 1 if budget > 1 else 0, min(budget // 2, 64), N=len(lengths), page=16, Hkv=2, d=64,
+             lengths=lengths)
+
+
+def test_graph_replay_follows_lengths():
+    for most in (600, 5000):
+        k, v, table, mass, pos = _case(23, N=2, page=16, Hkv=1, d=64, lengths=[most, most])
+        k0 = k.clone()
+        cache, mass, pos = dd.PagedCache(k, v, table.cuda()), mass.cuda(), pos.cuda()
+        lens = torch.tensor([most, most], dtype=torch.int32, device="cuda")
+        mo, po, src, no = torch.zeros_like(mass), torch.zeros_like(pos), torch.zeros_like(pos), torch.zeros_like(lens)
+        call = lambda: dd.dd_cache_evict(cache, lens, mass, pos, 256, mo, po, no, sink=2, recent=20, src=src)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        k.copy_(k0)
+        lens.copy_(torch.tensor([most - 7, 200], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert no.tolist() == [256, 200]
+        for n, length in enumerate(lens.tolist()):
+            want = OC.evict_one(mass[n, :length].cpu().numpy(), pos[n, :length].cpu().numpy(), 256, 2, 20)
+            assert src[n, :len(want)].tolist() == want
+
+
+def test_refusals_of_the_binding():
+    k, v, table, mass, pos = _case(24, N=2, page=16, Hkv=1, d=64, lengths=[60, 60])
+    cache, mass, pos = dd.PagedCache(k, v, table.cuda()), mass.cuda(), pos.cuda()
+    lens = torch.tensor([60, 60], dtype=torch.int32, device="cuda")
+
+    def call(**over):
+        a = dict(lengths=lens, mass=mass, pos=pos, budget=30, mass_out=torch.zeros_like(mass),
+                 pos_out=torch.zeros_like(pos), lengths_out=torch.zeros_like(lens))
+        a.update(over)
+        dd.dd_cache_evict(cache, **a)
+
+    call()
+    for over in (dict(mass=mass.double()), dict(mass=mass[:1]), dict(mass=mass.cpu()), dict(pos=pos.long()),
+                 dict(pos=pos[:, :-1]), dict(mass_out=mass[:, :10]), dict(lengths=lens.cpu()), dict(lengths=lens[:1]),
+                 dict(src=pos.long()), dict(mass=mass.t().contiguous().t())):
+        with pytest.raises((ValueError, TypeError)):
+            call(**over)
+    for over in (dict(budget=0), dict(sink=31), dict(mass_out=mass), dict(pos_out=pos), dict(lengths_out=lens),
+                 dict(max_len=100), dict(recent=-1)):
+        with pytest.raises(dd.DDError):
+            call(**over)

@@ -186,3 +186,123 @@ def test_beams_read_shared_pages():
     got = CC.run_attention(g)
     torch.cuda.synchronize()
     CC.check_attention(x, got, CC.attention_reference(x), BF16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 2), (7, 1), (16, 1), (34, 1), (32, 16)])
+@pytest.mark.parametrize("lengths,max_len", [([1], 1), ([64], 64), ([33], 64), ([65], 65), ([200], 300),
+                                             ([511], 512), ([0], 512), ([512, 0, 17], 512),
+                                             ([300, 5, 0, 64, 129] * 8, 300)])
+def test_short_sequences_without_masses(dtype, d, Hq, Hkv, lengths, max_len):
+    # one launch: a cluster for each sequence-head, or whole ones to a CTA
+    B = len(lengths)
+    holes = [(b, 0) for b, n in enumerate(lengths) if n > 40 and b % 3 == 0]
+    _check(20, B=B, Hq=Hq, Hkv=Hkv, d=d, page=16, lengths=lengths, max_len=max_len, dtype=dtype, holes=holes)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_whole_sequences_of_a_large_batch(dtype):
+    gen = np.random.default_rng(21)
+    lengths = gen.integers(0, 400, 100).tolist()
+    lengths[:3] = [0, 0, 512]
+    lengths[-1] = 0
+    _check(21, B=100, Hq=12, Hkv=4, d=64, page=24, lengths=lengths, max_len=512, dtype=dtype)
+
+
+def test_a_length_out_of_range_appends_nothing():
+    for mass in (False, True):
+        x = CC.make_attention(22, B=2, Hq=4, Hkv=2, d=64, page=16, lengths=[64, 30], mass=mass)
+        g = CC.on_gpu(x)
+        k0 = g["k"].clone()
+        g["lengths"][0] = 65
+        CC.run_attention(g)
+        assert dd.dd_get_device_error() == dd.DD_ERR_BOUNDS
+        page, row = int(x["table"][0, 3]), 15
+        assert torch.equal(g["k"][page, row], k0[page, row])
+        page, row = int(x["table"][1, 1]), 29 - 16
+        assert torch.equal(g["k"][page, row].cpu(), x["k_new"][1])
+
+
+def test_an_append_into_a_hole_is_dropped():
+    x = CC.make_attention(23, B=1, Hq=4, Hkv=2, d=64, page=16, lengths=[40], mass=True, holes=[(0, 2)])
+    _check(23, B=1, Hq=4, Hkv=2, d=64, page=16, lengths=[40], mass=True, holes=[(0, 2)])
+    _check(23, B=1, Hq=4, Hkv=2, d=64, page=16, lengths=[33], mass=False, holes=[(0, 2)])
+    assert int(x["table"][0, 2]) == -1
+
+
+@pytest.mark.parametrize("mass", [False, True])
+def test_two_calls_at_once(mass):
+    xs = [CC.make_attention(30 + i, B=6, Hq=16, Hkv=4, d=128, page=16, lengths=[900, 20, 700, 1, 350, 40],
+                            mass=mass) for i in range(2)]
+    gs = [CC.on_gpu(x) for x in xs]
+    want = [CC.run_attention(g) for g in gs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in gs]
+    n = dd.dd_paged_attention_workspace_size(6, 16, 4, 128, 900, mass)
+    spaces = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in gs]
+    torch.cuda.synchronize()
+    got = []
+    for rep in range(20):
+        got = [CC.run_attention(g, stream=s, workspace=w) for g, s, w in zip(gs, streams, spaces)]
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for key in a:
+            assert a[key] is None or torch.equal(a[key], b[key]), key
+
+
+def test_strided_rows():
+    # masses as columns of a wider table, new tokens as slices of a fused projection
+    x = CC.make_attention(40, B=3, Hq=8, Hkv=4, d=64, page=16, lengths=[100, 640, 7], mass=True)
+    g = CC.on_gpu(x)
+    B, M = g["mass"].shape
+    wide = torch.full((2, B, M + 5), 3.0, device="cuda")
+    wide[0, :, :M] = g["mass"]
+    fused = torch.zeros(B, 3 * 4 * 64, dtype=BF16, device="cuda")
+    fused[:, 256:512] = g["k_new"].view(B, -1)
+    fused[:, 512:] = g["v_new"].view(B, -1)
+    out, lse = torch.empty(B, 8, 64, dtype=BF16, device="cuda"), torch.empty(B, 8, device="cuda")
+    wide[1, :, :M] = g["mass"]
+    dd.dd_paged_attention(g["q"], dd.PagedCache(g["k"], g["v"], g["table"]), g["lengths"], out, lse,
+                          k_new=fused[:, 256:512].view(B, 4, 64), v_new=fused[:, 512:].view(B, 4, 64),
+                          mass=wide[0, :, :M], mass_out=wide[1, :, :M], max_len=x["max_len"])
+    torch.cuda.synchronize()
+    CC.check_attention(x, dict(out=out, lse=lse, mass=wide[1, :, :M]), CC.attention_reference(x), BF16)
+    assert torch.all(wide[:, :, M:] == 3.0)
+
+
+def test_refusals_of_the_binding():
+    x = CC.make_attention(41, B=2, Hq=4, Hkv=2, d=64, page=16, lengths=[20, 30], mass=True)
+    g = CC.on_gpu(x)
+    cache = dd.PagedCache(g["k"], g["v"], g["table"])
+    out, lse = torch.empty_like(g["q"]), torch.empty(2, 4, device="cuda")
+
+    def call(**over):
+        a = dict(q=g["q"], cache=cache, lengths=g["lengths"], out=out, lse=lse, k_new=g["k_new"],
+                 v_new=g["v_new"], mass=g["mass"], mass_out=torch.zeros_like(g["mass"]))
+        a.update(over)
+        dd.dd_paged_attention(a.pop("q"), a.pop("cache"), a.pop("lengths"), a.pop("out"), **a)
+
+    call()
+    bad = [dict(q=g["q"].float()), dict(q=g["q"].cpu()), dict(q=g["q"][:1]), dict(q=g["q"][:, :3]), dict(q=g["q"][..., :32]),
+           dict(q=g["q"].transpose(0, 1).contiguous().transpose(0, 1)), dict(lengths=g["lengths"].long()),
+           dict(lengths=g["lengths"][:1]), dict(lengths=g["lengths"].cpu()), dict(out=out.float()), dict(out=out[:, :2]),
+           dict(lse=lse.double()), dict(lse=lse[:, :2]), dict(k_new=None), dict(v_new=None), dict(k_new=g["k_new"].cpu()),
+           dict(k_new=g["k_new"][:, :1]), dict(mass_out=None), dict(mass=g["mass"][:, :-1]), dict(mass=g["mass"].double()),
+           dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)), dict(mass_out=torch.zeros(2, 60, device="cuda")[:, ::2])]
+    for over in bad:
+        with pytest.raises((ValueError, TypeError)):
+            call(**over)
+    for over in (dict(max_len=10 ** 6), dict(max_len=0), dict(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(dd.DDError):
+            call(**over)
+    for k, v, t in ((g["k"], g["v"].float(), g["table"]), (g["k"], g["v"][:, :8], g["table"]), (g["k"], g["v"], g["table"].long()),
+                    (g["k"], g["v"], g["table"].cpu()), (g["k"], g["v"], g["table"][0]), (g["k"][..., ::2], g["v"][..., ::2], g["table"]),
+                    (g["k"].half(), g["v"].half(), g["table"])):
+        with pytest.raises((ValueError, TypeError)):
+            dd.PagedCache(k, v, t)
+    call()
+    torch.cuda.synchronize()
+    assert dd.dd_get_device_error() == dd.DD_OK
