@@ -15,10 +15,15 @@ namespace dd {
 
 namespace {
 
-constexpr int kBeamThreads = 256;
+constexpr int kBeamThreads = 256;  // of the merge
 constexpr int kBeamWarps = kBeamThreads / 32;
-constexpr int kBeamVecs = 8;  // 16-byte vectors per thread: a segment of 128 bytes
-constexpr int kPieceBytes = kBeamThreads * kBeamVecs * 16;
+// The scan: pieces of 32 KB, six CTAs an SM, which is what bounds it: about 12 K cycles of
+// latency a piece (half of its issue slots are taken).
+constexpr int kScanThreads = 256;
+constexpr int kScanCtas = 6;       // an SM
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kScanVecs = 8;       // 16-byte vectors per thread: a segment of 128 bytes
+constexpr int kPieceBytes = kScanThreads * kScanVecs * 16;
 constexpr int kBeamList = 512;  // candidates ranked by counting
 constexpr uint32_t kNone = 0x007FFFFFu;  // key of -inf
 
@@ -70,13 +75,15 @@ __device__ __forceinline__ bool scans(const float* score_in, const uint8_t* done
 }
 
 // The largest 16-bit p that at least `want` of the block's keys reach, bit by bit; all threads
-// call it. (A barrier that counts costs 60 cycles a bit; one warp over all keys, 300 for two
-// bits.)
+// call it. (A barrier that counts costs 60 to 110 cycles a bit; one warp over all keys, 300
+// for two bits.)
+__device__ __forceinline__ void kth_bit(uint32_t key, int want, int bit, uint32_t& p) {
+  if (__syncthreads_count(key >= (p | (1u << bit))) >= want) p |= 1u << bit;
+}
 __device__ __forceinline__ uint32_t kth_key16(uint32_t key, int want) {
   uint32_t p = 0;
 #pragma unroll 1  // a kernel's first pass waits for its instructions: short code
-  for (int bit = 15; bit >= 0; --bit)
-    if (__syncthreads_count(key >= (p | (1u << bit))) >= want) p |= 1u << bit;
+  for (int bit = 15; bit >= 0; --bit) kth_bit(key, want, bit, p);
   return p;
 }
 
@@ -89,7 +96,7 @@ __device__ __forceinline__ uint32_t kth_key16(uint32_t key, int want) {
 // Where more than kBeamList logits reach the bound (long runs of equal logits), the K-th
 // largest is found by a radix select over the piece instead.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 6)
+__global__ void __launch_bounds__(kScanThreads, kScanCtas)
 beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pieces,
                  const float* __restrict__ score_in, const uint8_t* __restrict__ done_in,
                  float2* __restrict__ ml, uint2* __restrict__ cand, uint32_t spin) {
@@ -98,8 +105,8 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   extern __shared__ __align__(128) uint8_t piece_smem[];  // [kPieceBytes]
   __shared__ __align__(8) uint64_t bar;
   __shared__ uint2 s_list[kBeamList];   // (key, index in the piece)
-  __shared__ uint8_t s_seg[kBeamThreads];
-  __shared__ float2 s_ml[kBeamWarps + kBeamWarps / 2];  // and the radix select's scan
+  __shared__ uint8_t s_seg[kScanThreads];
+  __shared__ float2 s_ml[kScanWarps + kScanWarps / 2];  // and the radix select's scan
   __shared__ int s_n, s_segs, s_want;
   __shared__ uint32_t s_bound;
   const int row = blockIdx.x / pieces, piece = blockIdx.x - row * pieces;
@@ -121,14 +128,14 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   if (__syncthreads_or(!here)) return;  // recorded; uniform over the CTA
   if (n_here < kPiece) {
     T* x = reinterpret_cast<T*>(piece_smem);
-    for (int i = n_here + threadIdx.x; i < kPiece; i += kBeamThreads) x[i] = static_cast<T>(-INFINITY);
+    for (int i = n_here + threadIdx.x; i < kPiece; i += kScanThreads) x[i] = static_cast<T>(-INFINITY);
     __syncthreads();
   }
   const uint4* seg = reinterpret_cast<const uint4*>(piece_smem) + threadIdx.x;  // every 256th vector
   uint32_t mw[4] = {W::kNegInf, W::kNegInf, W::kNegInf, W::kNegInf};
 #pragma unroll
-  for (int i = 0; i < kBeamVecs; ++i) {
-    const uint4 v = seg[i * kBeamThreads];
+  for (int i = 0; i < kScanVecs; ++i) {
+    const uint4 v = seg[i * kScanThreads];
     mw[0] = max_word(mw[0], v.x, T{});
     mw[1] = max_word(mw[1], v.y, T{});
     mw[2] = max_word(mw[2], v.z, T{});
@@ -137,8 +144,8 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   float mx = max_of(max_word(max_word(mw[0], mw[1], T{}), max_word(mw[2], mw[3], T{}), T{}), T{}) + 0.f;
   if (mx == INFINITY) {  // not a candidate: again, without such logits
     mx = -INFINITY;
-    for (int i = 0; i < kBeamVecs; ++i) {
-      const uint4 v = seg[i * kBeamThreads];
+    for (int i = 0; i < kScanVecs; ++i) {
+      const uint4 v = seg[i * kScanThreads];
       const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -147,27 +154,38 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     }
   }
   const uint32_t mine = logit_key(mx) >> 16;
-  const uint32_t bound = kth_key16(mine, K);
+  uint32_t bound = 0;
   // sum of exponentials relative to the segment's maximum
   const float ref2 = mx * kLog2e;  // rounded once: the sum is relative to exactly 2^ref2
   const float ref = mx > -INFINITY ? ref2 : 0.f;
   float sum = 0.f;
   {
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int i = 0; i < kBeamVecs; ++i) {
-      const uint4 v = seg[i * kBeamThreads];
+    // two logits at a time: packed multiply-add and add; the bound's bits are counted in
+    // between, so that its barriers' latency is spent on them
+    float2 part[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[e] = make_float2(0.f, 0.f);
+    const float2 scale = make_float2(kLog2e, kLog2e), shift = make_float2(-ref, -ref);
+    static_assert(kScanVecs == 8);  // two of the 16 bits a vector
+#pragma unroll 1
+    for (int i = 0; i < kScanVecs; ++i) {
+      const uint4 v = seg[i * kScanThreads];
+      kth_bit(mine, K, 15 - 2 * i, bound);
       const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int h = 0; h < W::n; ++h) part[e] += fast_exp2(fmaf(W::get(r[e], h), kLog2e, -ref));
+      for (int e = 0; e < 4; e += 2 / W::n) {
+        const float2 x = W::n == 2 ? make_float2(W::get(r[e], 0), W::get(r[e], 1))
+                                   : make_float2(W::get(r[e], 0), W::get(r[e + 2 / W::n - 1], 0));
+        const float2 y = __ffma2_rn(x, scale, shift);
+        part[e] = __fadd2_rn(part[e], make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+      }
+      kth_bit(mine, K, 14 - 2 * i, bound);
     }
-    sum = (part[0] + part[1]) + (part[2] + part[3]);
+    sum = ((part[0].x + part[0].y) + (part[1].x + part[1].y)) + ((part[2].x + part[2].y) + (part[3].x + part[3].y));
     if (!(sum < INFINITY)) {  // NaN and +inf logits add nothing
       sum = 0.f;
-      for (int i = 0; i < kBeamVecs; ++i) {
-        const uint4 v = seg[i * kBeamThreads];
+      for (int i = 0; i < kScanVecs; ++i) {
+        const uint4 v = seg[i * kScanThreads];
         const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -189,21 +207,17 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   if (mine >= bound && mx > -INFINITY) s_seg[atomicAdd(&s_segs, 1)] = (uint8_t)threadIdx.x;
   __syncthreads();
   const int segs = s_segs;
-  for (int i = warp; i < segs; i += kBeamWarps) {
+  for (int i = warp; i < segs; i += kScanWarps) {
     const int t = s_seg[i];
-    // word `lane` of the segment: vector lane / 4, word lane % 4
-    const int at = (((lane >> 2) * kBeamThreads + t) << 2) + (lane & 3);
+    const int at = (((lane >> 2) * kScanThreads + t) << 2) + (lane & 3);
     const uint32_t w = words[at];
 #pragma unroll
     for (int h = 0; h < W::n; ++h) {
       const uint32_t k = logit_key(clean_logit(W::get(w, h)));
-      const bool in = (k >> 16) >= bound && k > kNone;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      if (!mask) continue;
-      int first = 0;
-      if (lane == 0) first = atomicAdd(&s_n, __popc(mask));
-      first = __shfl_sync(0xffffffffu, first, 0) + __popc(mask & ((1u << lane) - 1u));
-      if (in && first < kBeamList) s_list[first] = make_uint2(k, (uint32_t)(at * W::n + h));
+      if ((k >> 16) >= bound && k > kNone) {  // few do
+        const int place = atomicAdd(&s_n, 1);
+        if (place < kBeamList) s_list[place] = make_uint2(k, (uint32_t)(at * W::n + h));
+      }
     }
   }
   __syncthreads();
@@ -211,15 +225,15 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   if (n > kBeamList) {
     // ---- radix select over the piece
     int* hist = reinterpret_cast<int*>(s_list);  // the list is empty again
-    int* scan = reinterpret_cast<int*>(s_ml + kBeamWarps);
+    int* scan = reinterpret_cast<int*>(s_ml + kScanWarps);
     const T* x = reinterpret_cast<const T*>(piece_smem);
     uint32_t prefix = 0u;
     int want = K;
     for (int shift = 24; shift >= 0; shift -= 8) {
       const uint32_t hmask = shift == 24 ? 0u : (0xFFFFFFFFu << (shift + 8));
-      hist[threadIdx.x] = 0;
+      for (int i = threadIdx.x; i < 256; i += kScanThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = threadIdx.x; i < kPiece; i += kBeamThreads) {
+      for (int i = threadIdx.x; i < kPiece; i += kScanThreads) {
         const uint32_t k = logit_key(clean_logit((float)x[i]));
         if (k > kNone && (k & hmask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
       }
@@ -238,7 +252,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     // `want` >= 1 of the logits equal to it are taken, from the lowest index
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();  // also: the histogram is read
-    constexpr int kRun = kPiece / kBeamThreads;
+    constexpr int kRun = kPiece / kScanThreads;
     int ties = 0;
     for (int i = threadIdx.x * kRun; i < (threadIdx.x + 1) * kRun; ++i) {
       const uint32_t k = logit_key(clean_logit((float)x[i]));
@@ -268,7 +282,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     n = min(above + want, kBeamList);
   }
   uint2* out = cand + (int64_t)blockIdx.x * K;
-  for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+  for (int i = threadIdx.x; i < n; i += kScanThreads) {
     const uint2 c = s_list[i];
     int r = 0;
     for (int t = 0; t < n; ++t) {
@@ -277,14 +291,14 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     }
     if (r < K) out[r] = make_uint2(c.x, (uint32_t)base + c.y);
   }
-  for (int i = n + threadIdx.x; i < K; i += kBeamThreads) out[i] = make_uint2(kNone, 0u);
+  for (int i = n + threadIdx.x; i < K; i += kScanThreads) out[i] = make_uint2(kNone, 0u);
   if (threadIdx.x == 0) {
     m = s_ml[0].x;
 #pragma unroll
-    for (int w = 1; w < kBeamWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    for (int w = 1; w < kScanWarps; ++w) m = fmaxf(m, s_ml[w].x);
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kBeamWarps; ++w)
+    for (int w = 0; w < kScanWarps; ++w)
       if (s_ml[w].x > -INFINITY) s = fmaf(s_ml[w].y, fast_exp2(s_ml[w].x - m), s);
     ml[blockIdx.x] = make_float2(m, s);
   }
@@ -505,7 +519,7 @@ int beam_pieces(int V, dd_dtype dtype) {
 template <typename T>
 cudaError_t launch_scan(const BeamCall& p, unsigned grid, int pieces, float2* ml, uint2* cand,
                         cudaStream_t stream) {
-  beam_scan_kernel<T><<<grid, kBeamThreads, kPieceBytes, stream>>>(
+  beam_scan_kernel<T><<<grid, kScanThreads, kPieceBytes, stream>>>(
       static_cast<const T*>(p.logits), p.K, p.V, p.ld, pieces, p.score_in, p.done_in, ml, cand, spin_limit());
   return cudaGetLastError();
 }
