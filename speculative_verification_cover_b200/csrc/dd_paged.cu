@@ -13,7 +13,11 @@
 // Lengths are read on the device (a captured call follows them); only the launch
 // depends on max_len.
 //
-// Bound: HBM, 2 Hkv d elements per slot read once.
+// Bound: HBM, 2 Hkv d elements per slot read once. Measured (one B200, calls in a graph; of
+// the copy bandwidth): one sequence of 131071 slots, 8 kv heads of 128 bf16, 89 us (92%); 64
+// sequences of up to 8191, 4 kv heads, with masses, 111 us (75%; the scores' way to the join
+// and back is 58 of 600 MB); 7 of up to 2047, 32 kv heads, 26.6 us (71%): there the first
+// lengths, page ids and slots arriving, and the ends of sequence-heads, are a third of it.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -877,6 +881,8 @@ __device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2)
   m = mn;
 }
 
+// Bound: latency (4 us; with masses 6 us at 16 sequences of 1024 slots, 32 heads) and, with
+// masses in long caches, the scores' bytes (16 us at 64 sequences of up to 8191, 28 heads).
 // CTAs [0, B Hq): the output of one (sequence, query head) that was split, its parts over
 // four warps. The rest, mass_ctas to a sequence: the masses, from the scores the main
 // kernel left and the joined log-sums. Each warp takes eight heads at a time, forms their
