@@ -414,7 +414,8 @@ typedef struct {
  * out             [B,Hq,d] contiguous, dtype of q (required)
  * lse             [B,Hq] fp32, natural log (may be NULL)
  * mass_in, mass_out  [B, .] fp32, row stride mass_stride >= max_len. mass_out NULL: no
- *                 masses. mass_in NULL: zero. mass_in == mass_out adds in place. With
+ *                 masses. mass_in NULL: zero. mass_in == mass_out adds in place (they
+ *                 must not overlap in any other way). With
  *                 k_new, the appended slot's mass starts at 0 whatever mass_in holds
  *                 there. Slots at or beyond a sequence's length are not written.
  * workspace       device scratch of at least dd_paged_attention_workspace_size(...) bytes,

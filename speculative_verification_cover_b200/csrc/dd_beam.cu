@@ -326,7 +326,7 @@ __device__ __forceinline__ bool better(double s, int64_t at, double s2, int64_t 
 
 // What the merge holds in shared memory from its first loads: entries, and lists' sums (more
 // are read again where they are needed).
-constexpr int kHeldEntries = 3072;
+constexpr int kHeldEntries = 4096;
 constexpr int kHeldLists = 512;
 
 struct BeamOut {

@@ -857,7 +857,7 @@ struct Span {
 __device__ __forceinline__ Span split_of(const PagedArgs& a, int b, int pair) {
   Span s;
   const int p0 = a.prefix[b], p1 = a.prefix[b + 1];
-  const int share = (a.prefix[a.B] + a.grid - 1) / a.grid;
+  const int share = (int)(((uint32_t)a.prefix[a.B] + (uint32_t)a.grid - 1u) / (uint32_t)a.grid);
   s.tiles = (p1 - p0) / (a.c.Hkv * a.blocks);
   if (s.tiles == 0) return s;
   const int first = p0 + pair * s.tiles;

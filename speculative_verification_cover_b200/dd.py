@@ -448,11 +448,23 @@ def _call(name, gpu, stream, *args):
         raise DDError(name, st)
 
 
+def _overlaps(shape, stride):
+    """Whether two elements of a tensor may be one (an expanded view, say)."""
+    extent = 1
+    for st, n in sorted((st, n) for n, st in zip(shape, stride) if n > 1):
+        if st < extent:
+            return True
+        extent += st * (n - 1)
+    return False
+
+
 class PagedCache:
     """A paged K/V cache: k, v [pages, page_size, Hkv, d] or, for several layers that share
     page ids, [layers, pages, page_size, Hkv, d], and page_table [N, max_pages] int32.
     k and v have the same shape and strides, any strides with a unit last one (so a pool
-    stored heads first is passed as its transposed view). A page id below 0 is a hole."""
+    stored heads first is passed as its transposed view). A page id below 0 is a hole.
+    Pools whose elements share memory (expanded views, one tensor as both k and v) are
+    read only: calls that would write them are refused."""
 
     def __init__(self, k, v, page_table):
         gpu = _gpu(k, "k")
@@ -482,6 +494,7 @@ class PagedCache:
                               _dtype_code(k), page_table.data_ptr(),
                               page_table.stride(0) if self.N > 1 else self.max_pages, self.max_pages)
         self._ref = ctypes.byref(self._c)
+        self.read_only = k.data_ptr() == v.data_ptr() or _overlaps(k.shape, k.stride())
 
     def layer(self, i):
         """One layer's cache of a several-layer one (the same memory and page table)."""
@@ -498,6 +511,10 @@ class PagedCache:
             raise ValueError(f"the page table has {self.N} rows, the call {n} sequences")
         if gpu != self.gpu:
             raise ValueError(f"the cache is on cuda:{self.gpu}, the call's tensors on cuda:{gpu}")
+
+    def _written(self):
+        if self.read_only:
+            raise ValueError("elements of k and v share memory: the cache can only be read")
 
 
 def dd_paged_attention_workspace_size(B, Hq, Hkv, d, max_len, with_mass=False) -> int:
@@ -528,6 +545,7 @@ def dd_paged_attention(q, cache: PagedCache, lengths, out, lse=None, k_new=None,
     kp = vp = None
     ns = 0
     if k_new is not None or v_new is not None:
+        cache._written()
         kp, ns = _rows(k_new, "k_new", dtype, (B, Hkv, d), gpu)
         vp, vs = _rows(v_new, "v_new", dtype, (B, Hkv, d), gpu)
         if ns != vs and B > 1:
@@ -568,6 +586,7 @@ def dd_cache_evict(cache: PagedCache, lengths, mass, pos, budget, mass_out, pos_
     shape = mass.shape
     N, M = shape
     cache._fits(N, gpu)
+    cache._written()
     max_len = min(M, cache.slots) if max_len is None else int(max_len)
     i32, f32 = torch.int32, torch.float32
     mi = _arg(mass, "mass", f32, shape, gpu)
@@ -637,7 +656,7 @@ def dd_beam_reorder(parent, states, stream=None):
         if sp < dp + size and dp < sp + size:
             raise ValueError("src and dst of a state must not overlap")
         x.src, x.dst = sp, dp
-        x.row_bytes = x.src_stride = x.dst_stride = size // n
+        x.row_bytes = x.src_stride = x.dst_stride = size // n if n else 0
     _call("dd_beam_reorder", gpu, stream, _arg(parent, "parent", torch.int32, (B, K), gpu), B, K, c, len(states))
 
 
@@ -652,6 +671,7 @@ def dd_paged_fork(cache: PagedCache, parent, lengths, fresh, table_out, lengths_
     B, K = parent.shape
     n = B * K
     cache._fits(n, gpu)
+    cache._written()
     i32 = torch.int32
     pp = _arg(parent, "parent", i32, (B, K), gpu)
     lp = _arg(lengths, "lengths", i32, (n,), gpu)

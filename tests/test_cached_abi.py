@@ -169,3 +169,12 @@ def test_page_division_is_exact(n):
               (2 ** 31 - 1) // n * n - 1, 2 ** 30, 12345}:
         if 0 <= x < 2 ** 31:
             assert x * m < 1 << 64 and (x * m) >> (31 + l) == x // n, x
+
+
+@pytest.mark.parametrize("shape,stride,shared", [
+    ((3, 4, 2, 64), (512, 128, 64, 1), False), ((3, 4, 2, 64), (512, 64, 256, 1), False),
+    ((3, 4, 2, 64), (4096, 128, 64, 1), False), ((1, 4, 1, 64), (0, 64, 0, 1), False),
+    ((3, 4, 2, 64), (0, 128, 64, 1), True), ((3, 4, 2, 64), (512, 128, 0, 1), True),
+    ((3, 4, 2, 64), (256, 128, 64, 1), True), ((3, 4, 2, 64), (512, 64, 64, 1), True)])
+def test_pools_whose_elements_share_memory(shape, stride, shared):
+    assert dd._overlaps(shape, stride) is shared

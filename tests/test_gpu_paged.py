@@ -306,3 +306,36 @@ def test_refusals_of_the_binding():
     call()
     torch.cuda.synchronize()
     assert dd.dd_get_device_error() == dd.DD_OK
+
+
+def test_pools_that_share_memory_are_read_only():
+    """One key head expanded to all heads (or one tensor as keys and values) can be attended
+    to; what would write it is refused."""
+    x = CC.make_attention(21, B=2, Hq=4, Hkv=2, d=64, page=8, lengths=[9, 20], append=False)
+    x["k"], x["v"] = (t[:, :, :1].expand(-1, -1, 2, -1) for t in (x["k"], x["v"]))
+    g = {n: t.cuda() if isinstance(t, torch.Tensor) else t for n, t in x.items()}
+    g["k"], g["v"] = (x[n][:, :, :1].contiguous().cuda().expand(-1, -1, 2, -1) for n in ("k", "v"))
+    assert g["k"].stride(2) == 0
+    got = CC.run_attention(g)
+    torch.cuda.synchronize()
+    CC.check_attention(x, got, CC.attention_reference(x), BF16)
+    cache = dd.PagedCache(g["k"], g["v"], g["table"])
+    new = torch.zeros(2, 2, 64, dtype=BF16, device="cuda")
+    out, parent = torch.empty_like(g["q"]), torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    n, f = g["lengths"], torch.zeros(2, 20, device="cuda")
+    i = torch.zeros(2, 20, dtype=torch.int32, device="cuda")
+    k = torch.zeros(8, 8, 2, 64, dtype=BF16, device="cuda")
+    for c in (cache, dd.PagedCache(k, k, g["table"])):
+        assert c.read_only
+        with pytest.raises(ValueError, match="only be read"):
+            dd.dd_paged_attention(g["q"], c, n, out, k_new=new, v_new=new)
+        with pytest.raises(ValueError, match="only be read"):
+            dd.dd_cache_evict(c, n, f, i, 5, f.clone(), i.clone(), n.clone())
+        with pytest.raises(ValueError, match="only be read"):
+            dd.dd_paged_fork(c, parent, n, n.clone(), torch.empty_like(g["table"]), n.clone())
+
+
+def test_empty_batches_are_refused():
+    i = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    with pytest.raises(dd.DDError):
+        dd.dd_beam_reorder(i, [(torch.zeros(0, 3, device="cuda"), torch.zeros(0, 3, device="cuda"))])
