@@ -1,6 +1,7 @@
 """Build libdd.so in place with nvcc for sm_100a (B200), and beside it
 libdd_checked.so, the same source with the device index checks compiled in
-(DD_CHECK_BOUNDS; include/dd.h, dd_bounds_checked).
+(DD_CHECK_BOUNDS; include/dd.h, dd_bounds_checked), and _args.so, the binding's
+argument checks (host code).
 
     python -m speculative_verification_cover_b200.build [--force] [-v]
 """
@@ -10,11 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdd.so")
 OUT_CHECKED = os.path.join(HERE, "libdd_checked.so")
+OUT_ARGS = os.path.join(HERE, "_args.so")
+ARGS_SOURCE = os.path.join(CSRC, "dd_args.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -41,12 +45,23 @@ def up_to_date(out: str = OUT) -> bool:
     if not os.path.exists(out):
         return False
     t = os.path.getmtime(out)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    return all(os.path.getmtime(s) <= t for s in ([ARGS_SOURCE] if out == OUT_ARGS else sources()))
+
+
+def _args_command(out):
+    """g++ for the binding's argument checks, which read torch's tensors."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I" + sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-o", out, ARGS_SOURCE, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile whichever of the two libraries is missing or older than a source
-    (both at once), and return the path of libdd.so."""
+    """Compile whichever of the two libraries and the binding's _args.so is missing or older
+    than a source (all at once), and return the path of libdd.so."""
     jobs = []
     for out, extra in ((OUT, []), (OUT_CHECKED, ["-DDD_CHECK_BOUNDS"])):
         if not force and up_to_date(out):
@@ -57,6 +72,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         jobs.append((subprocess.Popen(cmd), tmp, out, cmd))
+    if force or not up_to_date(OUT_ARGS):
+        cmd = _args_command(OUT_ARGS + ".tmp")
+        jobs.append((subprocess.Popen(cmd), OUT_ARGS + ".tmp", OUT_ARGS, cmd))
     failed = None
     for proc, tmp, out, cmd in jobs:
         if proc.wait() != 0:

@@ -367,8 +367,8 @@ def dd_decide(policy, tokens, is_seed, eligible, stats: RowStats, pos_offset, de
 # Every tensor of a call is checked here -- device, type, shape, layout -- before its
 # address reaches the library; the call runs on that device, on `stream` (None: its
 # current stream), and a workspace that is not given is allocated for that stream. A
-# decode step makes many small calls, so the checks are one expression a tensor, and what
-# is wrong is looked for only once something is.
+# decode step makes many small calls, so a tensor's checks are one compiled call
+# (csrc/dd_args.cpp), and what is wrong is looked for only once something is.
 def _gpu(t, name):
     """Index of the device a call runs on: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
@@ -390,26 +390,35 @@ def _refuse(t, name, dtype, shape, gpu, rows):
     raise ValueError(f"{name} must be contiguous" + (" within a row" if rows else ""))
 
 
+_host = None  # csrc/dd_args.cpp: the checks, and the library's calls without ctypes
+
+
+def _load_host():
+    """Load the binding's compiled part and give it the library's entry points."""
+    global _host, _arg, _rows
+    L = lib()
+    try:
+        from . import _args
+    except ImportError as e:
+        raise ImportError(f"{e}: build it with `python -m speculative_verification_cover_b200.build`") from e
+    _args.set_refuse(_refuse)
+    for name in ("dd_paged_attention", "dd_cache_evict", "dd_beam_select", "dd_beam_reorder", "dd_paged_fork"):
+        getattr(_args, "bind_" + name)(ctypes.cast(getattr(L, name), ctypes.c_void_p).value)
+    _arg, _rows, _host = _args.arg, _args.rows, _args
+    return _args
+
+
 def _arg(t, name, dtype, shape, gpu):
     """Address of a contiguous tensor of the given type, shape and device."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _refuse(t, name, dtype, shape, gpu, False)
+    _load_host()
+    return _arg(t, name, dtype, shape, gpu)
 
 
 def _rows(t, name, dtype, shape, gpu):
     """Address and row stride of a tensor whose rows (all dimensions but the first) are
     contiguous."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == gpu:
-            if t.is_contiguous() or (t.shape[0] > 1 and t[0].is_contiguous()):
-                return t.data_ptr(), t.stride(0)
-    except AttributeError:
-        pass
-    _refuse(t, name, dtype, shape, gpu, True)
+    _load_host()
+    return _rows(t, name, dtype, shape, gpu)
 
 
 def _scratch(nbytes, gpu, stream):
@@ -423,18 +432,19 @@ def _scratch(nbytes, gpu, stream):
 
 def _workspace(t, gpu):
     """Address and bytes of a caller's workspace."""
+    got = (_host or _load_host()).workspace(t, gpu)
+    if got is not None:
+        return got
     if not isinstance(t, torch.Tensor):
         raise TypeError("workspace: expected a torch.Tensor")
     if t.get_device() != gpu:
         raise ValueError(f"workspace is on {t.device}, the call's other tensors on cuda:{gpu}")
-    if not t.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return t.data_ptr(), t.numel() * t.element_size()
+    raise ValueError("workspace must be contiguous")
 
 
 def _call(name, gpu, stream, *args):
     """A library call on device `gpu` (made current only where it is not), on `stream`."""
-    fn = getattr(_lib or lib(), name)
+    fn = getattr(_host or _load_host(), name)
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(gpu)
     else:
@@ -493,7 +503,7 @@ class PagedCache:
                               self.layers, self.n_pages, self.page_size, self.Hkv, self.d,
                               _dtype_code(k), page_table.data_ptr(),
                               page_table.stride(0) if self.N > 1 else self.max_pages, self.max_pages)
-        self._ref = ctypes.byref(self._c)
+        self._ref = ctypes.addressof(self._c)  # lives as long as the cache
         self.read_only = k.data_ptr() == v.data_ptr() or _overlaps(k.shape, k.stride())
 
     def layer(self, i):
@@ -634,9 +644,6 @@ def dd_beam_select(logits, score, parent, token, score_out, done=None, done_out=
           do, wp, wb)
 
 
-_ROW_STATES = [_RowState * max(1, n) for n in range(17)]
-
-
 def dd_beam_reorder(parent, states, stream=None):
     """States follow their parents: parent [B,K] int32; states: up to 8 pairs (src, dst) of
     tensors [B*K, ...] or [B,K,...], contiguous, of the same shape and dtype."""
@@ -645,19 +652,18 @@ def dd_beam_reorder(parent, states, stream=None):
         raise ValueError("parent must be [B, K]")
     B, K = parent.shape
     n = B * K
-    c = _ROW_STATES[min(len(states), 16)]()
-    for x, (src, dst) in zip(c, states):
+    rows = []
+    for src, dst in states:
         shape = src.shape
         sp = _arg(src, "src", src.dtype, shape, gpu)
         dp = _arg(dst, "dst", src.dtype, shape, gpu)
-        if shape[0] != n and shape[:2] != (B, K):
+        if len(shape) < 1 or shape[0] != n and (len(shape) < 2 or shape[0] != B or shape[1] != K):
             raise ValueError(f"a state must be [B*K, ...] or [B, K, ...], got {tuple(shape)}")
-        size = src.numel() * src.element_size()
+        size = src.nbytes
         if sp < dp + size and dp < sp + size:
             raise ValueError("src and dst of a state must not overlap")
-        x.src, x.dst = sp, dp
-        x.row_bytes = x.src_stride = x.dst_stride = size // n if n else 0
-    _call("dd_beam_reorder", gpu, stream, _arg(parent, "parent", torch.int32, (B, K), gpu), B, K, c, len(states))
+        rows += (sp, dp, size // n if n else 0)
+    _call("dd_beam_reorder", gpu, stream, _arg(parent, "parent", torch.int32, (B, K), gpu), B, K, rows)
 
 
 def dd_paged_fork(cache: PagedCache, parent, lengths, fresh, table_out, lengths_out, stream=None):

@@ -178,3 +178,57 @@ def test_page_division_is_exact(n):
     ((3, 4, 2, 64), (256, 128, 64, 1), True), ((3, 4, 2, 64), (512, 64, 64, 1), True)])
 def test_pools_whose_elements_share_memory(shape, stride, shared):
     assert dd._overlaps(shape, stride) is shared
+
+
+def test_compiled_argument_checks(lib):
+    """The binding's compiled checks (gpu -1 stands for the CPU here): addresses and strides,
+    and an error that says what is wrong."""
+    f32, cpu = torch.float32, -1
+    t = torch.zeros(3, 4, 5)
+    wide = torch.zeros(3, 32)
+    assert dd._arg(t, "t", f32, (3, 4, 5), cpu) == t.data_ptr()
+    assert dd._arg(torch.nn.Parameter(t), "t", f32, t.shape, cpu) == t.data_ptr()
+    assert dd._rows(t, "t", f32, t.shape, cpu) == (t.data_ptr(), 20)
+    assert dd._rows(wide[:, 2:7], "w", f32, (3, 5), cpu) == (wide.data_ptr() + 8, 32)
+    assert dd._rows(wide[:, :20].unflatten(1, (4, 5)), "w", f32, (3, 4, 5), cpu) == (wide.data_ptr(), 32)
+    assert dd._rows(wide[:1, 2:7], "w", f32, (1, 5), cpu)[0] == wide.data_ptr() + 8
+    assert dd._arg(t[:0], "t", f32, (0, 4, 5), cpu) == 0
+    with pytest.raises(TypeError, match="name_of_it: expected a torch.Tensor"):
+        dd._arg([1.0], "name_of_it", f32, (1,), cpu)
+    with pytest.raises(TypeError):
+        dd._arg(None, "t", f32, (1,), cpu)
+    for bad in ((torch.int32, (3, 4, 5)), (f32, (3, 4)), (f32, (3, 4, 6)), (f32, (3, 4, 5, 1)), (f32, ())):
+        with pytest.raises(ValueError, match="must be torch"):
+            dd._arg(t, "t", *bad, cpu)
+        with pytest.raises(ValueError, match="must be torch"):
+            dd._rows(t, "t", *bad, cpu)
+    with pytest.raises(ValueError, match="cuda:0"):
+        dd._arg(t, "t", f32, t.shape, 0)
+    for view in (t.transpose(0, 1), t[:, ::2], t[..., :3]):
+        for check in (dd._arg, dd._rows):
+            with pytest.raises(ValueError, match="must be contiguous"):
+                check(view, "t", f32, view.shape, cpu)
+    with pytest.raises(ValueError, match="must be contiguous"):
+        dd._arg(wide[:, 2:7], "w", f32, (3, 5), cpu)
+    assert dd._workspace(wide, cpu) == (wide.data_ptr(), 3 * 32 * 4)
+    for bad, error in ((wide[:, :4], ValueError), (b"ws", TypeError)):
+        with pytest.raises(error):
+            dd._workspace(bad, cpu)
+    with pytest.raises(ValueError):
+        dd._workspace(wide, 0)
+
+
+def test_compiled_calls_check_their_arguments(lib):
+    host = dd._host or dd._load_host()
+    assert host.dd_cache_evict(None, None, 0, 0, 1, 0, 0, None, None, 0, *[None] * 5) == dd.DD_ERR_INVALID_ARG
+    assert host.dd_beam_reorder(FAKE, 2, 4, [], None) == dd.DD_ERR_INVALID_ARG
+    assert host.dd_beam_reorder(FAKE, 2, 4, [FAKE, OTHER, 8] * 9, None) == dd.DD_ERR_UNSUPPORTED
+    assert host.dd_beam_reorder(FAKE, 2, 4, [FAKE, OTHER, 8, OTHER, OTHER, 8], None) == dd.DD_ERR_INVALID_ARG
+    with pytest.raises(TypeError):
+        host.dd_cache_evict(None)
+    with pytest.raises(TypeError):
+        host.dd_beam_reorder(FAKE, 2, 4, (), None)
+    with pytest.raises(OverflowError):
+        host.dd_beam_reorder(FAKE, 2 ** 31, 4, [], None)
+    with pytest.raises(TypeError):
+        host.dd_beam_reorder(FAKE, 2, "4", [], None)
