@@ -35,7 +35,7 @@ constexpr int kPagedThreads = 128;
 constexpr int kPagedWarps = kPagedThreads / 32;
 constexpr int kMaxPagedGrid = 1024;  // bounds the workspace on any device
 constexpr int kMaxHeads = 16;    // query heads of one block at most
-constexpr int kWholeLen = 512;   // sequences up to here are not split (without masses)
+constexpr int kWholeLen = 512;   // sequences up to here are not split
 constexpr int kPairCtas = 8;     // CTAs of a sequence-head's cluster (few short sequences)
 
 // How the tiles are given to CTAs: equal ranges, joined by a second kernel; whole
@@ -852,19 +852,22 @@ paged_fp32_kernel(const __grid_constant__ PagedArgs a) {
 // ------------------------------------------------------------------ join and masses
 // CTAs whose tiles hold a sequence-head: first and last, from the plan of the main kernel.
 struct Span {
-  int c0, c1, tiles;
+  int c0, c1;
 };
-__device__ __forceinline__ Span split_of(const PagedArgs& a, int b, int pair) {
-  Span s;
-  const int p0 = a.prefix[b], p1 = a.prefix[b + 1];
-  const int share = (int)(((uint32_t)a.prefix[a.B] + (uint32_t)a.grid - 1u) / (uint32_t)a.grid);
-  s.tiles = (p1 - p0) / (a.c.Hkv * a.blocks);
-  if (s.tiles == 0) return s;
-  const int first = p0 + pair * s.tiles;
-  s.c0 = first / share;
-  s.c1 = (first + s.tiles - 1) / share;
-  return s;
-}
+// What the plan says of a sequence: its first tile, the tiles of each of its heads (or head
+// blocks), and the tiles of a CTA.
+struct SequenceTiles {
+  int first, tiles, share;
+  __device__ __forceinline__ SequenceTiles(const PagedArgs& a, int b) {
+    first = a.prefix[b];
+    tiles = (a.prefix[b + 1] - first) / (a.c.Hkv * a.blocks);
+    share = (int)(((uint32_t)a.prefix[a.B] + (uint32_t)a.grid - 1u) / (uint32_t)a.grid);
+  }
+  __device__ __forceinline__ Span span(int pair) const {
+    const int at = first + pair * tiles;
+    return Span{at / share, (at + tiles - 1) / share};
+  }
+};
 __device__ __forceinline__ int64_t part_slot(const Span& s, int c) {
   return 2 * (int64_t)c + (c == s.c0 ? 1 : 0);
 }
@@ -883,27 +886,28 @@ __device__ __forceinline__ void merge_ml(float& m, float& l, float m2, float l2)
 
 // Bound: latency (4 us; with masses 6 us at 16 sequences of 1024 slots, 32 heads) and, with
 // masses in long caches, the scores' bytes (16 us at 64 sequences of up to 8191, 28 heads).
-// CTAs [0, B Hq): the output of one (sequence, query head) that was split, its parts over
-// four warps. The rest, mass_ctas to a sequence: the masses, from the scores the main
-// kernel left and the joined log-sums. Each warp takes eight heads at a time, forms their
-// log-sums (4 lanes to a head) rather than waiting for another kernel's, and adds up their
-// part of the CTA's slots.
+// CTAs [0, out_ctas = B Hq, or none where no sequence-head is split): the output of one
+// (sequence, query head) that was split, its parts over four warps. The rest, mass_ctas to a
+// sequence: the masses, from the scores the main kernel left and the joined log-sums. Each
+// warp takes eight heads at a time, forms their log-sums (4 lanes to a head) rather than
+// waiting for another kernel's, and adds up their part of the CTA's slots.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
+paged_join_kernel(const __grid_constant__ PagedArgs a, int out_ctas, int mass_ctas) {
   pdl_wait();
   constexpr int N = D / 32;
   extern __shared__ float z2[];  // [Hq rounded up to 8] of this sequence, log2 units (mass CTAs);
                                 // a warp's heads are written and read by that warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t heads = (int64_t)a.B * a.Hq;
-  if (blockIdx.x < heads) {
+  if (blockIdx.x < out_ctas) {
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     __shared__ float s_o[kJoinWarps][D];
     const int i = blockIdx.x, b = i / a.Hq, h = i - b * a.Hq;
     const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
-    const Span s = split_of(a, b, kvh * a.blocks + blk);
-    if (s.tiles == 0 || s.c0 == s.c1) return;  // already whole
+    const SequenceTiles plan(a, b);
+    if (plan.tiles == 0) return;
+    const Span s = plan.span(kvh * a.blocks + blk);
+    if (s.c0 == s.c1) return;  // already whole
     float m = -INFINITY, l = 0.f, acc[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[e] = 0.f;
@@ -959,7 +963,7 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
     return;
   }
   // ---- masses of one sequence's slots
-  const int k = (int)(blockIdx.x - heads), b = k / mass_ctas, part = k - b * mass_ctas;
+  const int k = (int)(blockIdx.x - out_ctas), b = k / mass_ctas, part = k - b * mass_ctas;
   const int len = checked_length(a.lengths, b, a.max_len);
   if (part * kMassChunk >= len) return;
   __shared__ float4 s_sum[kJoinWarps][32];
@@ -974,32 +978,40 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, int mass_ctas) {
         x[e] = *reinterpret_cast<const float4*>(scores + min(h + e, a.Hq - 1) * a.score_row + j);
   };
   load(8 * warp);
-  for (int h0 = 8 * warp; h0 < a.Hq; h0 += 8 * kJoinWarps) {
-    const int h = h0 + (lane >> 2);
-    float m = -INFINITY, l = 0.f;
-    bool whole = false;
-    if (h < a.Hq) {
-      const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
-      const Span s = split_of(a, b, kvh * a.blocks + blk);
-      whole = s.c0 == s.c1;
-      if (whole) {
-        m = a.lse2[(int64_t)b * a.Hq + h];
-      } else {
+  // a head without weights (or behind the last) adds none: e^{s - inf} = 0
+  if (a.split != PagedSplit::kRanges) {  // whole heads: four times this warp's eight at once
+    for (int h = 8 * warp + (lane & 7) + 8 * kJoinWarps * (lane >> 3); h < (a.Hq + 7) / 8 * 8; h += 32 * kJoinWarps) {
+      const float m = h < a.Hq ? a.lse2[(int64_t)b * a.Hq + h] : -INFINITY;
+      z2[h] = m == -INFINITY ? INFINITY : m;
+    }
+  } else {
+    const SequenceTiles plan(a, b);
+    for (int h0 = 8 * warp; h0 < a.Hq; h0 += 8 * kJoinWarps) {
+      const int h = h0 + (lane >> 2);
+      float m = -INFINITY, l = 0.f;
+      bool whole = false;
+      if (h < a.Hq) {
+        const int kvh = h / a.G, g = h - kvh * a.G, blk = g / a.heads, gi = g - blk * a.heads;
+        const Span s = plan.span(kvh * a.blocks + blk);
+        whole = s.c0 == s.c1;
+        if (whole) {
+          m = a.lse2[(int64_t)b * a.Hq + h];
+        } else {
 #pragma unroll 4
-        for (int c = s.c0 + (lane & 3); c <= s.c1; c += 4) {
-          const float2 ml = a.part_ml[part_slot(s, c) * a.heads + gi];
-          merge_ml(m, l, ml.x, ml.y);
+          for (int c = s.c0 + (lane & 3); c <= s.c1; c += 4) {
+            const float2 ml = a.part_ml[part_slot(s, c) * a.heads + gi];
+            merge_ml(m, l, ml.x, ml.y);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-      if (!whole) merge_ml(m, l, m2, l2);
+      for (int o = 1; o < 4; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        if (!whole) merge_ml(m, l, m2, l2);
+      }
+      if ((lane & 3) == 0)
+        z2[h] = h >= a.Hq || m == -INFINITY ? INFINITY : whole ? m : m + log2f(l);
     }
-    // a head without weights (or behind the last) adds none: e^{s - inf} = 0
-    if ((lane & 3) == 0)
-      z2[h] = h >= a.Hq || m == -INFINITY ? INFINITY : whole ? m : m + log2f(l);
   }
   __syncwarp();
   const float inv = 1.f / (float)a.Hq;
@@ -1198,19 +1210,32 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   a.lse2 = reinterpret_cast<float*>(ws + w.lse2);
   a.score_row = score_row(p.max_len);
   a.scores = p.mass_out ? reinterpret_cast<float*>(ws + w.scores) : nullptr;
-  // Short sequences take one launch, with nothing left to a join. With as many sequence-heads
-  // as SMs whole ones fill the GPU (64 sequences of 4 kv heads, 512 slots: 15.1 us, 19.5 split;
-  // 8 kv heads, 256 slots: 16.9, 18.5); with few, a CTA would walk through its tiles alone (one
-  // sequence of 8 kv heads, 200 slots: 8.2 us whole, 6.7 split and joined) and a cluster shares
-  // them (6.2 us, and 2 us less of the host's time than two launches), unless there is one tile
-  // (64 slots: 5.1 us whole, 6.2 split). Clusters beyond what is resident at once would queue:
-  // those are split (8 sequences, 256 slots: 7.7 us; whole 8.5).
+  // Short sequences are not split, so that nothing is left to a join (with masses: but those).
+  // Whole sequence-heads fill the GPU where there are as many as SMs and not a few more than
+  // CTAs at once, whose second round runs on a nearly idle GPU; what that costs is compared with
+  // the join, about four tiles of a CTA (none with masses: their join stays), or small against
+  // eight rounds. fp32 with masses is bound by its issue slots, which ragged whole ones leave
+  // idle (64 of 4, 100 to 512 slots: 37.5, 32.4 split): short ones only. (bf16, 28 heads: 64 sequences of 4 kv heads, 512 slots:
+  // 15.1 us, 19.5 split; with masses 17.5, 20.6; of 100 to 250, 96 of them: 14.4, 19.0. 64 of 8,
+  // 256 slots: 15.5, 18.5; but 512 slots: 22.4, 19.6 split. fp32: 64 of 4, 250 slots:
+  // 13.4, 15.5; 64 of 8, 512 slots: 39.6, 33.4 split; 96 of 32, 1 to 400 slots: 148, 160.) With few, a CTA would walk through its
+  // tiles alone (one sequence of 8 kv heads, 200 slots: 8.2 us whole, 6.7 split and joined) and a
+  // cluster shares them (6.2 us, and 2 us less of the host's time than two launches), unless there
+  // is one tile (64 slots: 5.1 us whole, 6.2 split). With masses, which take a second launch
+  // anyway, a cluster gains nothing (200 slots: 8.2 us, 7.8 split). Clusters beyond what is
+  // resident at once would queue: those are split (8 sequences, 256 slots: 7.7 us; whole 8.5).
   a.split = PagedSplit::kRanges;
-  if (!p.mass_out && p.max_len <= kWholeLen) {
-    const int64_t pairs = sequence_heads(a);
-    if (pairs >= device_info().sm_count || p.max_len <= kTileSlots) a.split = PagedSplit::kWhole;
-    else if (pairs * kPairCtas <= 2 * device_info().sm_count) a.split = PagedSplit::kCluster;
-  }
+  const int tile = c.d * e == 512 ? kTileSlots / 2 : kTileSlots;
+  const int64_t pairs = sequence_heads(a), sms = device_info().sm_count;
+  const int64_t resident = sms * (c.dtype == DD_BF16 && a.heads <= 8 ? 3 : 2);
+  const int64_t idle = pairs <= resident ? 0 : (resident - pairs % resident) % resident;
+  const int whole_len = p.mass_out && c.dtype == DD_F32 ? 4 * tile : kWholeLen;
+  const bool even = pairs >= 8 * resident ||
+                    idle * tile_count(p.max_len, tile) <= (p.mass_out ? 0 : 4 * resident);
+  if (p.max_len <= tile || (p.max_len <= whole_len && pairs >= sms && even))
+    a.split = PagedSplit::kWhole;
+  else if (p.max_len <= kWholeLen && !p.mass_out && pairs * kPairCtas <= 2 * sms)
+    a.split = PagedSplit::kCluster;
   cudaError_t err;
   if (c.dtype == DD_BF16)
     err = c.d == 128 ? launch_bf16<128>(a, stream) : launch_bf16<64>(a, stream);
@@ -1218,18 +1243,19 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
     err = c.d == 128 ? launch_fp32<128, true>(a, stream) : launch_fp32<64, true>(a, stream);
   else
     err = c.d == 128 ? launch_fp32<128, false>(a, stream) : launch_fp32<64, false>(a, stream);
-  if (err != cudaSuccess || a.split != PagedSplit::kRanges) return err;
-  // join: a CTA per query head; masses: enough CTAs a sequence to fill the GPU a few times
+  if (err != cudaSuccess || (a.split != PagedSplit::kRanges && !p.mass_out)) return err;
+  // join: a CTA per query head that may be split; masses: enough CTAs a sequence to fill the GPU a few times
   int mass_ctas = 0;
   if (p.mass_out) {
     const int chunks = (p.max_len + kMassChunk - 1) / kMassChunk;
     const int fill = (device_info().sm_count * 8 + p.B - 1) / p.B;
     mass_ctas = chunks < fill ? chunks : fill;
   }
-  const dim3 grid((unsigned)(p.B * p.Hq + mass_ctas * p.B));
+  const int out_ctas = a.split == PagedSplit::kRanges ? p.B * p.Hq : 0;
+  const dim3 grid((unsigned)(out_ctas + mass_ctas * p.B));
   const size_t zmem = p.mass_out ? ((size_t)p.Hq + 7) / 8 * 8 * 4 : 0;
   const auto join = [&](auto kernel) {
-    return launch_dependent(kernel, grid, dim3(kJoinThreads), zmem, stream, a, mass_ctas);
+    return launch_dependent(kernel, grid, dim3(kJoinThreads), zmem, stream, a, out_ctas, mass_ctas);
   };
   if (c.dtype == DD_BF16)
     return c.d == 128 ? join(paged_join_kernel<__nv_bfloat16, 128>)

@@ -339,3 +339,15 @@ def test_empty_batches_are_refused():
     i = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
     with pytest.raises(dd.DDError):
         dd.dd_beam_reorder(i, [(torch.zeros(0, 3, device="cuda"), torch.zeros(0, 3, device="cuda"))])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B,Hq,Hkv,lengths", [
+    (1, 256, 32, [12]), (40, 80, 8, [1, 4, 0, 3]), (160, 4, 1, [128, 1, 77, 0]), (80, 6, 2, [120, 512, 300, 5]),
+    (64, 8, 8, [200, 512]), (130, 16, 4, [33, 64, 2])])
+def test_masses_of_short_sequences(dtype, B, Hq, Hkv, lengths):
+    """Whole sequence-heads, with the masses from their own log-sums: more heads than a warp
+    takes at once, empty sequences, pages that are holes, all rounds of CTAs."""
+    lengths = (lengths * B)[:B]
+    holes = [(b, 0) for b in range(0, B, 7) if lengths[b] > 8]
+    _check(24, B=B, Hq=Hq, Hkv=Hkv, d=64, page=8, lengths=lengths, dtype=dtype, mass=True, holes=holes)
