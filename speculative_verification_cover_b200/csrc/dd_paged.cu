@@ -1215,15 +1215,16 @@ cudaError_t launch_paged_attention(const PagedCall& p, cudaStream_t stream) {
   // CTAs at once, whose second round runs on a nearly idle GPU; what that costs is compared with
   // the join, about four tiles of a CTA (none with masses: their join stays), or small against
   // eight rounds. fp32 with masses is bound by its issue slots, which ragged whole ones leave
-  // idle (64 of 4, 100 to 512 slots: 37.5, 32.4 split): short ones only. (bf16, 28 heads: 64 sequences of 4 kv heads, 512 slots:
-  // 15.1 us, 19.5 split; with masses 17.5, 20.6; of 100 to 250, 96 of them: 14.4, 19.0. 64 of 8,
-  // 256 slots: 15.5, 18.5; but 512 slots: 22.4, 19.6 split. fp32: 64 of 4, 250 slots:
-  // 13.4, 15.5; 64 of 8, 512 slots: 39.6, 33.4 split; 96 of 32, 1 to 400 slots: 148, 160.) With few, a CTA would walk through its
-  // tiles alone (one sequence of 8 kv heads, 200 slots: 8.2 us whole, 6.7 split and joined) and a
-  // cluster shares them (6.2 us, and 2 us less of the host's time than two launches), unless there
-  // is one tile (64 slots: 5.1 us whole, 6.2 split). With masses, which take a second launch
-  // anyway, a cluster gains nothing (200 slots: 8.2 us, 7.8 split). Clusters beyond what is
-  // resident at once would queue: those are split (8 sequences, 256 slots: 7.7 us; whole 8.5).
+  // idle (64 of 4, 100 to 512 slots: 37.5, 32.4 split): short ones only. (bf16, 28 heads: 64
+  // sequences of 4 kv heads, 512 slots: 15.1 us, 19.5 split; with masses 17.5, 20.6; of 100 to
+  // 250, 96 of them: 14.4, 19.0. 64 of 8, 256 slots: 15.5, 18.5; but 512 slots: 22.4, 19.6
+  // split. fp32: 64 of 4, 250 slots: 13.4, 15.5; 64 of 8, 512 slots: 39.6, 33.4 split; 96 of 32,
+  // 1 to 400 slots: 148, 160.) With few, a CTA would walk through its tiles alone (one sequence
+  // of 8 kv heads, 200 slots: 8.2 us whole, 6.7 split and joined) and a cluster shares them (6.2
+  // us, and 2 us less of the host's time than two launches), unless there is one tile (64 slots:
+  // 5.1 us whole, 6.2 split). With masses, which take a second launch anyway, a cluster gains
+  // nothing (200 slots: 8.2 us, 7.8 split). Clusters beyond what is resident at once would
+  // queue: those are split (8 sequences, 256 slots: 7.7 us; whole 8.5).
   a.split = PagedSplit::kRanges;
   const int tile = c.d * e == 512 ? kTileSlots / 2 : kTileSlots;
   const int64_t pairs = sequence_heads(a), sms = device_info().sm_count;
