@@ -479,9 +479,11 @@ dd_status dd_cache_evict(
  *   a beam that is done (done_in) has the one candidate (k, eos) at its own score,
  *   a beam whose score_in is not finite has none (an empty slot: -inf).
  * The K best of the K V candidates, by score; equal scores: the lower beam, then the larger
- * logit, then the lower token. Scores are compared in 64 bits (the sum's error, about 1e-7, is what can order two beams'
- * candidates wrongly). A logit that is not finite (-inf: a banned token) is no candidate and
- * adds nothing to the sum. Where there are fewer than K candidates the rest get
+ * logit, then the lower token. Scores are compared in 64 bits (the sum's error, about 1e-7,
+ * is what can order two beams' candidates wrongly). A logit that is not finite (-inf: a banned
+ * token) is no candidate and adds nothing to the sum. A finite one of any size, the type's
+ * lowest value among them, is a candidate like any other; a score below fp32's range is
+ * stored as -inf. Where there are fewer than K candidates the rest get
  * parent -1, token -1, score -inf, done 0.
  *
  * logits          [B,K,V], row stride ld >= V, DD_F32 or DD_BF16, 16-byte aligned,

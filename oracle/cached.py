@@ -97,8 +97,8 @@ def beam_candidates(logits, score, done, eos, V, most):
         if not live.any():
             continue
         m = x[live].max()
-        lse = m + np.log(np.exp(x[live] - m).sum())
-        values.append(base + (x[live] - lse))
+        # relative to m: next to logits of 1e30 a log-sum is lost even in 64 bits
+        values.append(base + ((x[live] - m) - np.log(np.exp(x[live] - m).sum())))
         places.append(k * V + np.nonzero(live)[0])
         beams.append(np.full(int(live.sum()), k))
         logit.append(x[live])

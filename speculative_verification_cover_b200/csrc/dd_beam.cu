@@ -1,6 +1,7 @@
 // Beam search's selection over beams and vocabulary (dd_beam_select).
 //
-// score(k, v) = score_k + x_kv - lse_k with lse_k = log sum_u e^{x_ku}. Within a beam the
+// score(k, v) = score_k + x_kv - lse_k with lse_k = log sum_u e^{x_ku}, summed and compared
+// relative to the beam's largest logit: (x_kv - m_k) - log sum_u e^{x_ku - m_k}. Within a beam the
 // order of the candidates is the order of the logits, so the scan of a row needs no lse:
 // each CTA reads one piece of one row once, leaves the piece's maximum, its sum of
 // exponentials and its K best logits, and a merge CTA per request joins the sums and picks
@@ -157,13 +158,14 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   }
   const uint32_t mine = logit_key(mx) >> 16;
   uint32_t bound = 0;
-  // sum of exponentials relative to the segment's maximum
-  const float ref2 = mx * kLog2e;  // rounded once: the sum is relative to exactly 2^ref2
-  const float ref = mx > -INFINITY ? ref2 : 0.f;
+  // sum of exponentials relative to the segment's maximum. The maximum is subtracted before
+  // the change of base: a difference below 0, exact to half a step of its own, whatever the
+  // logits' size, where log2(e) times a logit may overflow or lose all that lies between two.
+  const float ref = mx > -INFINITY ? mx : 0.f;
   float sum = 0.f;
   {
-    // two logits at a time: packed multiply-add and add; the bound's bits are counted in
-    // between, so that its barriers' latency is spent on them
+    // two logits at a time, packed; the bound's bits are counted in between, so that its
+    // barriers' latency is spent on them
     float2 part[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[e] = make_float2(0.f, 0.f);
@@ -178,7 +180,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
       for (int e = 0; e < 4; e += 2 / W::n) {
         const float2 x = W::n == 2 ? make_float2(W::get(r[e], 0), W::get(r[e], 1))
                                    : make_float2(W::get(r[e], 0), W::get(r[e + 2 / W::n - 1], 0));
-        const float2 y = __ffma2_rn(x, scale, shift);
+        const float2 y = __fmul2_rn(__fadd2_rn(x, shift), scale);
         part[e] = __fadd2_rn(part[e], make_float2(fast_exp2(y.x), fast_exp2(y.y)));
       }
       kth_bit(mine, K, 14 - 2 * i, bound);
@@ -193,15 +195,15 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
         for (int e = 0; e < 4; ++e)
 #pragma unroll
           for (int h = 0; h < W::n; ++h)
-            sum += fast_exp2(fmaf(clean_logit(W::get(r[e], h)), kLog2e, -ref));
+            sum += fast_exp2((clean_logit(W::get(r[e], h)) - ref) * kLog2e);
       }
     }
   }
-  // (maximum, sum) of the piece, log2 units
-  float m = ref2;
+  // (maximum, sum) of the piece
+  float m = mx;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  sum *= mx > -INFINITY ? fast_exp2(ref2 - m) : 0.f;
+  sum *= mx > -INFINITY ? fast_exp2((mx - m) * kLog2e) : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_ml[warp] = make_float2(m, sum);
@@ -301,7 +303,7 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kScanWarps; ++w)
-      if (s_ml[w].x > -INFINITY) s = fmaf(s_ml[w].y, fast_exp2(s_ml[w].x - m), s);
+      if (s_ml[w].x > -INFINITY) s = fmaf(s_ml[w].y, fast_exp2((s_ml[w].x - m) * kLog2e), s);
     ml[blockIdx.x] = make_float2(m, s);
   }
 }
@@ -394,7 +396,7 @@ beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     double z = 0.0;
     if (m > -INFINITY)
-      for (int i = lane; i < pieces; i += 32) z += (double)p[i].y * (double)exp2f(p[i].x - m);
+      for (int i = lane; i < pieces; i += 32) z += (double)p[i].y * (double)expf(p[i].x - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (lane == 0) {
@@ -405,14 +407,15 @@ beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
   __syncthreads();
   if (threadIdx.x < K && s_kind[threadIdx.x] == 1) {
     const float m = s_max[threadIdx.x];
-    if (m > -INFINITY) s_base[threadIdx.x] -= (double)m * (1.0 / (double)kLog2e) + log(s_sum[threadIdx.x]);
+    if (m > -INFINITY) s_base[threadIdx.x] -= log(s_sum[threadIdx.x]);
     else s_kind[threadIdx.x] = 0;
   }
   __syncthreads();
-  // an entry of live beam k; the one candidate of done beam k
+  // An entry of live beam k, from its distance to the beam's largest logit (next to which score
+  // and log-sum may be lost in 64 bits); the one candidate of done beam k.
   const auto entry = [&](int k, const uint2& c, double& s, int64_t& at) {
     if (s_kind[k] != 1 || c.x <= kNone) return false;
-    s = s_base[k] + (double)key_logit(c.x);
+    s = s_base[k] + ((double)key_logit(c.x) - (double)s_max[k]);
     at = place_of(k, c.x, (int)c.y);
     return true;
   };

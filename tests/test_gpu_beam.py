@@ -277,3 +277,77 @@ def test_refusals_of_the_binding():
         dd.dd_beam_reorder(parent, [])
     with pytest.raises(dd.DDError):
         dd.dd_beam_reorder(parent, [(s, s.clone())] * 9)
+
+
+def _check_range(logits, score, done=None, eos=-1):
+    """_check for scores that fp32 may not hold: what lies below its range is -inf."""
+    got = _select(logits, score, done, eos)
+    x = logits.float().cpu().numpy()
+    for b in range(x.shape[0]):
+        dn = None if done is None else done[b].cpu().numpy()
+        parent, token, out, ended = OC.beam_select(x[b], score[b].cpu().numpy(), dn, eos)
+        assert got[0][b].tolist() == parent.tolist(), b
+        assert got[1][b].tolist() == token.tolist(), b
+        assert got[3][b].tolist() == ended.tolist(), b
+        with np.errstate(over="ignore"):
+            want = out.astype(np.float32).astype(np.float64)
+        fin = np.isfinite(want)
+        assert np.array_equal(got[2][b][~fin], want[~fin])
+        assert np.all(np.abs(got[2][b][fin] - out[fin]) <= 2.0 ** -24 * np.abs(out[fin]) + 1e-6)
+
+
+def _masked(x, where, mask):
+    """x with the logits of a pattern at the mask's value: eight vectors of 16 bytes, every 256th
+    of a piece of 32 KB, are one thread's segment; 32 such segments a warp's."""
+    V, per = x.shape[-1], 16 // x.element_size()
+    i = torch.arange(V, device=x.device)
+    thread, piece = i // per % 256, i // (per * 2048)
+    hit = {"segment": (thread == 7) & (piece == 0), "warp": (thread // 32 == 1) & (piece == 0), "piece": piece == 0,
+           "all but one": i != V // 3, "all but twenty": i % (V // 20) != 0, "row": i >= 0}[where]
+    return torch.where(hit, mask, x.float()).to(x.dtype)
+
+
+MASKS = [lambda f: f.min, lambda f: -f.max / 2, lambda f: -1e38, lambda f: -1e30, lambda f: -1e20, lambda f: -1e10,
+         lambda f: -3e9, lambda f: -65504.0]
+
+
+@pytest.mark.parametrize("mask", range(len(MASKS)))
+@pytest.mark.parametrize("where", ["segment", "warp", "piece", "all but one", "all but twenty", "row"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_finite_masks(dtype, where, mask):
+    """Tokens banned by a large negative finite value, in one beam and in all of them."""
+    value = MASKS[mask](torch.finfo(dtype))
+    for V in (1000, 20000):
+        wide, score = _logits(30, 2, 5, V, dtype)
+        x = wide.clone()
+        x[:, 2] = _masked(x[:, 2], where, value)
+        _check_range(x, score)
+        x = _masked(wide, where, value)
+        _check_range(x, score)
+        done = torch.zeros(2, 5, dtype=torch.uint8, device="cuda")
+        done[:, 3] = 1
+        _check_range(x, score, done, eos=5)
+        # no logit of the row left, or some
+        x[0, 1] = float("-inf")
+        x[1, 4, ::2] = float("-inf")
+        _check_range(x, score)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_finite_logits(dtype):
+    f = torch.finfo(dtype)
+    for best in (1e5, 1e10, 1e30, f.max / 2, f.max):
+        for V in (1000, 20000):
+            x, score = _logits(31, 2, 4, V, dtype)
+            x[:, torch.arange(4), torch.arange(4) * 7 + 3] = torch.tensor(best, dtype=dtype, device="cuda")
+            _check_range(x, score)          # each beam's best; the rest far behind
+            x[0, 1] = f.min
+            x[1, :, V // 2:] = f.min
+            _check_range(x, score)
+            score[:, 1:] = float("-inf")    # one beam: its other tokens are all that follows
+            _check_range(x, score)
+    # a whole row at the largest value, one of it at the lowest: every distance overflows
+    x, score = _logits(32, 1, 3, 9000, dtype)
+    x[0, 0], x[0, 1], x[0, 2] = f.max, f.min, f.max
+    x[0, 2, 1::2] = f.min
+    _check_range(x, score)
