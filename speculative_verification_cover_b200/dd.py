@@ -573,6 +573,8 @@ def dd_paged_attention(q, cache: PagedCache, lengths, out, lse=None, k_new=None,
             ms = rows[1]
         if max_len is None:
             max_len = min(cache.slots, rows[1])
+        elif max_len > rows[1]:  # the library sees the row stride alone, which may be larger
+            raise DDError("dd_paged_attention", DD_ERR_INVALID_ARG)
     elif mass is not None:
         raise ValueError("mass without mass_out")
     max_len = cache.slots if max_len is None else int(max_len)

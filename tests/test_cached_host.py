@@ -1,0 +1,40 @@
+"""Host side of the cached operators' binding, without a GPU: the checks of CPU tensors (in
+the place of a device's) up to the library's call, which is recorded and not made."""
+import pytest
+import torch
+
+from speculative_verification_cover_b200 import build, dd
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    build.build()
+    made = []
+    monkeypatch.setattr(dd, "_gpu", lambda t, name: -1)  # what the compiled checks call the CPU
+    monkeypatch.setattr(dd, "_call", lambda name, gpu, stream, *args: made.append((name, args)))
+    return made
+
+
+def _cache(N=2, pages=8, page=16, Hkv=2, d=64, width=8):
+    k, v = (torch.zeros(pages, page, Hkv, d) for _ in range(2))
+    return dd.PagedCache(k, v, torch.zeros(N, width, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("B", [1, 2, 3])
+def test_masses_narrower_than_max_len_are_refused(calls, B):
+    """Masses may be columns of a wider buffer: a max_len above their width would have the
+    call write what lies behind them."""
+    cache = _cache(N=B)
+    q, n = torch.zeros(B, 4, 64), torch.zeros(B, dtype=torch.int32)
+    wide = torch.zeros(B, 128)
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    call = lambda **kw: dd.dd_paged_attention(q, cache, n, torch.zeros_like(q), workspace=ws, **kw)
+    call(mass_out=wide[:, :50], max_len=50)
+    call(mass=wide[:, :50], mass_out=wide[:, :50], max_len=7)
+    call(mass_out=wide[:, :50])
+    assert [c[1][9] for c in calls] == [50, 7, 50]  # max_len as the library gets it
+    for kw in (dict(mass_out=wide[:, :50], max_len=51), dict(mass_out=wide[:, :50], max_len=128),
+               dict(mass=wide[:, 50:60], mass_out=wide[:, :10], max_len=11)):
+        with pytest.raises(dd.DDError):
+            call(**kw)
+    assert len(calls) == 3
