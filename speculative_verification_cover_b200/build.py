@@ -1,12 +1,13 @@
 """Build libdd.so in place with nvcc for sm_100a (B200), and beside it
 libdd_checked.so, the same source with the device index checks compiled in
-(DD_CHECK_BOUNDS; include/dd.h, dd_bounds_checked), and _args.so, the binding's
-argument checks (host code).
+(DD_CHECK_BOUNDS; include/dd.h, dd_bounds_checked), and the binding's compiled
+part (host code; args_path()).
 
     python -m speculative_verification_cover_b200.build [--force] [-v]
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -17,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdd.so")
 OUT_CHECKED = os.path.join(HERE, "libdd_checked.so")
-OUT_ARGS = os.path.join(HERE, "_args.so")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "dd.h")
 ARGS_SOURCE = os.path.join(CSRC, "dd_args.cpp")
 
 NVCC_FLAGS = [
@@ -37,15 +38,21 @@ def _nvcc():
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                  if f.endswith((".cu", ".cuh", ".h"))) + [
-        os.path.join(os.path.dirname(HERE), "include", "dd.h")]
+                  if f.endswith((".cu", ".cuh", ".h"))) + [HEADER]
+
+
+def args_path() -> str:
+    """The binding's compiled part. It reads Python's and torch's objects, so one that was built
+    for another Python or torch has another name and is not found."""
+    return os.path.join(HERE, f"_args.{sysconfig.get_config_var('SOABI')}-torch{importlib.metadata.version('torch')}.so")
 
 
 def up_to_date(out: str = OUT) -> bool:
     if not os.path.exists(out):
         return False
     t = os.path.getmtime(out)
-    return all(os.path.getmtime(s) <= t for s in ([ARGS_SOURCE] if out == OUT_ARGS else sources()))
+    # the binding's part calls the library by the header's signatures
+    return all(os.path.getmtime(s) <= t for s in ([ARGS_SOURCE, HEADER] if out == args_path() else sources()))
 
 
 def _args_command(out):
@@ -60,8 +67,8 @@ def _args_command(out):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile whichever of the two libraries and the binding's _args.so is missing or older
-    than a source (all at once), and return the path of libdd.so."""
+    """Compile whichever of the two libraries and the binding's compiled part is missing or
+    older than a source (all at once), and return the path of libdd.so."""
     jobs = []
     for out, extra in ((OUT, []), (OUT_CHECKED, ["-DDD_CHECK_BOUNDS"])):
         if not force and up_to_date(out):
@@ -72,9 +79,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         jobs.append((subprocess.Popen(cmd), tmp, out, cmd))
-    if force or not up_to_date(OUT_ARGS):
-        cmd = _args_command(OUT_ARGS + ".tmp")
-        jobs.append((subprocess.Popen(cmd), OUT_ARGS + ".tmp", OUT_ARGS, cmd))
+    args = args_path()
+    if force or not up_to_date(args):
+        cmd = _args_command(args + ".tmp")
+        jobs.append((subprocess.Popen(cmd), args + ".tmp", args, cmd))
     failed = None
     for proc, tmp, out, cmd in jobs:
         if proc.wait() != 0:

@@ -12,10 +12,13 @@ index checks (see dd_bounds_checked in include/dd.h).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass, fields
 
 import torch
+
+from . import build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdd.so")
@@ -397,10 +400,12 @@ def _load_host():
     """Load the binding's compiled part and give it the library's entry points."""
     global _host, _arg, _rows
     L = lib()
-    try:
-        from . import _args
-    except ImportError as e:
-        raise ImportError(f"{e}: build it with `python -m speculative_verification_cover_b200.build`") from e
+    path = build.args_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with "
+                          "`python -m speculative_verification_cover_b200.build`")
+    spec = importlib.util.spec_from_file_location(__package__ + "._args", path)
+    _args = importlib.util.module_from_spec(spec)
     _args.set_refuse(_refuse)
     for name in ("dd_paged_attention", "dd_cache_evict", "dd_beam_select", "dd_beam_reorder", "dd_paged_fork"):
         getattr(_args, "bind_" + name)(ctypes.cast(getattr(L, name), ctypes.c_void_p).value)

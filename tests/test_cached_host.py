@@ -1,5 +1,8 @@
 """Host side of the cached operators' binding, without a GPU: the checks of CPU tensors (in
 the place of a device's) up to the library's call, which is recorded and not made."""
+import importlib.metadata
+import os
+
 import pytest
 import torch
 
@@ -38,3 +41,24 @@ def test_masses_narrower_than_max_len_are_refused(calls, B):
         with pytest.raises(dd.DDError):
             call(**kw)
     assert len(calls) == 3
+
+
+def test_the_binding_s_part_is_rebuilt_for_its_header_python_and_torch(monkeypatch):
+    """It has the header's signatures compiled in, and reads torch's tensors."""
+    path = build.args_path()
+    build.build()
+    assert os.path.exists(path) and build.up_to_date(path)
+    times = {path: 1.0, build.HEADER: 2.0}
+    with monkeypatch.context() as m:
+        m.setattr(os.path, "getmtime", lambda p: times.get(p, 0.0))
+        assert not build.up_to_date(path)
+        times[build.HEADER] = 1.0
+        assert build.up_to_date(path)
+        times[build.ARGS_SOURCE] = 2.0
+        assert not build.up_to_date(path)
+    with monkeypatch.context() as m:
+        m.setattr(importlib.metadata, "version", lambda name: "0.0")
+        assert build.args_path() != path and not build.up_to_date(build.args_path())
+        m.setattr(dd, "_host", None)
+        with pytest.raises(ImportError, match="torch0.0"):
+            dd._load_host()
