@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -44,7 +45,11 @@ def sources():
 def args_path() -> str:
     """The binding's compiled part. It reads Python's and torch's objects, so one that was built
     for another Python or torch has another name and is not found."""
-    return os.path.join(HERE, f"_args.{sysconfig.get_config_var('SOABI')}-torch{importlib.metadata.version('torch')}.so")
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "none"
+    return os.path.join(HERE, f"_args.{sysconfig.get_config_var('SOABI')}-torch{torch_version}.so")
 
 
 def up_to_date(out: str = OUT) -> bool:
@@ -66,9 +71,17 @@ def _args_command(out):
             "-o", out, ARGS_SOURCE, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def _left_out(args, e):
+    if os.path.exists(args):  # older than its sources: not to be called
+        os.remove(args)
+    warnings.warn(f"the binding's compiled part was not built, without it the cached-decoding calls raise ImportError: {e}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile whichever of the two libraries and the binding's compiled part is missing or
-    older than a source (all at once), and return the path of libdd.so."""
+    older than a source (all at once), and return the path of libdd.so. Without Python's or
+    torch's headers the binding's part is left out with a warning: the libraries and the
+    verification step's calls do without it, the cached-decoding calls say what is missing."""
     jobs = []
     for out, extra in ((OUT, []), (OUT_CHECKED, ["-DDD_CHECK_BOUNDS"])):
         if not force and up_to_date(out):
@@ -81,12 +94,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
         jobs.append((subprocess.Popen(cmd), tmp, out, cmd))
     args = args_path()
     if force or not up_to_date(args):
-        cmd = _args_command(args + ".tmp")
-        jobs.append((subprocess.Popen(cmd), args + ".tmp", args, cmd))
+        try:
+            cmd = _args_command(args + ".tmp")
+            jobs.append((subprocess.Popen(cmd), args + ".tmp", args, cmd))
+        except (ImportError, OSError) as e:  # no torch, no compiler
+            _left_out(args, e)
     failed = None
     for proc, tmp, out, cmd in jobs:
         if proc.wait() != 0:
-            failed = failed or subprocess.CalledProcessError(proc.returncode, cmd)
+            e = subprocess.CalledProcessError(proc.returncode, cmd)
+            if out == args:
+                _left_out(args, e)
+            else:
+                failed = failed or e
         else:
             os.replace(tmp, out)
     if failed:

@@ -62,3 +62,27 @@ def test_the_binding_s_part_is_rebuilt_for_its_header_python_and_torch(monkeypat
         m.setattr(dd, "_host", None)
         with pytest.raises(ImportError, match="torch0.0"):
             dd._load_host()
+
+
+@pytest.mark.parametrize("missing", ["compiler", "headers", "torch"])
+def test_libraries_build_without_the_binding_s_part(monkeypatch, tmp_path, missing):
+    """The verification step and the C ABI need nvcc alone."""
+    build.build()
+    part = str(tmp_path / "part.so")
+    monkeypatch.setattr(build, "args_path", lambda: part)
+    if missing == "torch":
+        def command(out):
+            raise ImportError("No module named 'torch'")
+        monkeypatch.setattr(build, "_args_command", command)
+    else:
+        monkeypatch.setenv("CXX", "false" if missing == "headers" else str(tmp_path / "no_such_compiler"))
+    for old in (False, True):
+        if old:  # one that is older than its sources does not stay
+            open(part, "w").close()
+            os.utime(part, (0, 0))
+        with pytest.warns(UserWarning, match="not built"):
+            assert build.build() == build.OUT
+        assert not os.path.exists(part)
+    monkeypatch.setattr(dd, "_host", None)
+    with pytest.raises(ImportError, match="is missing: build it"):
+        dd._load_host()
