@@ -487,7 +487,7 @@ dd_status dd_cache_evict(
  * parent -1, token -1, score -inf, done 0.
  *
  * logits          [B,K,V], row stride ld >= V, DD_F32 or DD_BF16, 16-byte aligned,
- *                 ld * element a multiple of 16 bytes
+ *                 ld * element a multiple of 16 bytes; nothing behind a row's V is read
  * score_in        [B,K] fp32; done_in [B,K] u8 or NULL (none); eos in [-1, V), -1: no token
  *                 ends a beam (a done beam then gets token -1)
  * parent, token   [B,K] int32; score_out [B,K] fp32 in descending order (not score_in's memory);

@@ -117,23 +117,29 @@ beam_scan_kernel(const T* __restrict__ logits, int K, int V, int64_t ld, int pie
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int base = piece * kPiece, n_here = min(kPiece, V - base);
   uint32_t* words = reinterpret_cast<uint32_t*>(piece_smem);
+  const T* from = logits + (int64_t)row * ld + base;
+  // whole vectors by the bulk copy, the logits of a last, partly filled one by threads: nothing
+  // is read behind the vocabulary
+  const int copied = n_here & ~(16 / (int)sizeof(T) - 1);
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
     tc::fence_barrier_init();
-    const uint32_t bytes = ((uint32_t)n_here * sizeof(T) + 15u) & ~15u;
-    tc::mbar_expect_tx(&bar, bytes);
-    tc::bulk_load(piece_smem, logits + (int64_t)row * ld + base, bytes, &bar);
+    if (copied > 0) {
+      const uint32_t bytes = (uint32_t)copied * sizeof(T);
+      tc::mbar_expect_tx(&bar, bytes);
+      tc::bulk_load(piece_smem, from, bytes, &bar);
+    }
     s_n = 0;
     s_segs = 0;
   }
-  __syncthreads();
-  const bool here = mbar_wait_bounded(&bar, 0, spin);
-  if (__syncthreads_or(!here)) return;  // recorded; uniform over the CTA
   if (n_here < kPiece) {
     T* x = reinterpret_cast<T*>(piece_smem);
-    for (int i = n_here + threadIdx.x; i < kPiece; i += kScanThreads) x[i] = static_cast<T>(-INFINITY);
-    __syncthreads();
+    for (int i = copied + threadIdx.x; i < kPiece; i += kScanThreads)
+      x[i] = i < n_here ? from[i] : static_cast<T>(-INFINITY);
   }
+  __syncthreads();
+  const bool here = copied == 0 || mbar_wait_bounded(&bar, 0, spin);
+  if (__syncthreads_or(!here)) return;  // recorded; uniform over the CTA
   const uint4* seg = reinterpret_cast<const uint4*>(piece_smem) + threadIdx.x;  // every 256th vector
   uint32_t mw[4] = {W::kNegInf, W::kNegInf, W::kNegInf, W::kNegInf};
 #pragma unroll

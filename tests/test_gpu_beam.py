@@ -351,3 +351,18 @@ def test_large_finite_logits(dtype):
     x[0, 0], x[0, 1], x[0, 2] = f.max, f.min, f.max
     x[0, 2, 1::2] = f.min
     _check_range(x, score)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 9, 15, 1001, 8191, 8193, 16385, 20001])
+def test_a_contiguous_row_that_ends_its_storage(dtype, V):
+    """One beam's logits, unpadded: the last, partly filled 16 bytes are the row's own alone."""
+    gen = torch.Generator().manual_seed(33)
+    x = torch.randn(1, 1, V, generator=gen).to(dtype).cuda()
+    x[..., -1] = 9.0
+    got = _check(x, torch.zeros(1, 1, device="cuda"))
+    assert int(got[1][0, 0]) == V - 1
+    # what lies behind a row of a wider buffer is not read: the largest there is, right behind
+    wide = torch.full((2, 3, -(-(V + 1) // 8) * 8), torch.finfo(dtype).max, dtype=dtype, device="cuda")
+    wide[..., :V] = torch.randn(2, 3, V, generator=gen).to(dtype).cuda()
+    _check(wide[..., :V], torch.tensor([[0.0, -1.0, -2.5], [-0.3, -1.1, -2.0]], device="cuda"))
