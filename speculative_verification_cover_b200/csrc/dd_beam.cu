@@ -419,9 +419,9 @@ beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
   __syncthreads();
   // An entry of live beam k, from its distance to the beam's largest logit (next to which score
   // and log-sum may be lost in 64 bits); the one candidate of done beam k.
-  const auto entry = [&](int k, const uint2& c, double& s, int64_t& at) {
-    if (s_kind[k] != 1 || c.x <= kNone) return false;
-    s = s_base[k] + ((double)key_logit(c.x) - (double)s_max[k]);
+  const auto entry = [&](int k, double base, double largest, const uint2& c, double& s, int64_t& at) {
+    if (c.x <= kNone) return false;
+    s = base + ((double)key_logit(c.x) - largest);
     at = place_of(k, c.x, (int)c.y);
     return true;
   };
@@ -437,10 +437,12 @@ beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
     int64_t at;
 #pragma unroll 1
     for (int k = warp; k < K; k += kBeamWarps) {
-      if (s_kind[k] == 1)
+      if (s_kind[k] == 1) {
+        const double base = s_base[k], largest = s_max[k];
 #pragma unroll 2
         for (int i = k * per_beam + lane; i < (k + 1) * per_beam; i += 32)
-          if (entry(k, i < kHeldEntries ? s_cand[i] : mine[i], s, at)) f(s, at);
+          if (entry(k, base, largest, i < kHeldEntries ? s_cand[i] : mine[i], s, at)) f(s, at);
+      }
       if (lane == 0 && ended(k, s, at)) f(s, at);
     }
   };
@@ -490,7 +492,8 @@ beam_merge_kernel(int K, int pieces, const float* __restrict__ score_in,
       const int k = i / pieces, h = head[i];
       double s;
       int64_t at;
-      if (s_kind[k] == 1 ? h < K && entry(k, mine[i * K + h], s, at) : h == 0 && i == k * pieces && ended(k, s, at))
+      if (s_kind[k] == 1 ? h < K && entry(k, s_base[k], s_max[k], mine[i * K + h], s, at)
+                         : h == 0 && i == k * pieces && ended(k, s, at))
         if (better(s, at, o.score, o.at)) o = Best{s, at, i};
     }
   };
