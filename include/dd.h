@@ -372,7 +372,11 @@ dd_status dd_select_seeds_ex(
  * error found on the device: it records DD_ERR_BOUNDS, the page counts as a hole, the
  * length is clamped (and nothing is appended to such a sequence).
  * Strides are in elements and whole multiples of 16 bytes; k and v are 16-byte
- * aligned. page_size is any number from 1 on. */
+ * aligned. page_size is any number from 1 on.
+ *
+ * In each of these calls an output, or the workspace, that shares memory with an input or
+ * another output is DD_ERR_INVALID_ARG (what a call says may be in place excepted). Rows of
+ * one array may lie between those of another. The pools themselves are not compared. */
 typedef struct {
   void* k;
   void* v;
@@ -411,13 +415,12 @@ typedef struct {
  * max_len         bound on lengths, at most max_pages * page_size; sizes the launch and
  *                 the workspace, not the result.
  * softmax_scale   <= 0 selects 1/sqrt(d)
- * out             [B,Hq,d] contiguous, dtype of q (required)
+ * out             [B,Hq,d] contiguous, dtype of q (required); q itself, if that is contiguous
  * lse             [B,Hq] fp32, natural log (may be NULL)
  * mass_in, mass_out  [B, .] fp32, row stride mass_stride >= max_len. mass_out NULL: no
- *                 masses. mass_in NULL: zero. mass_in == mass_out adds in place (they
- *                 must not overlap in any other way). With
- *                 k_new, the appended slot's mass starts at 0 whatever mass_in holds
- *                 there. Slots at or beyond a sequence's length are not written.
+ *                 masses. mass_in NULL: zero. mass_in == mass_out adds in place. With k_new,
+ *                 the appended slot's mass starts at 0 whatever mass_in holds there.
+ *                 Slots at or beyond a sequence's length are not written.
  * workspace       device scratch of at least dd_paged_attention_workspace_size(...) bytes,
  *                 256-byte aligned; contents on entry are ignored. Calls that share a
  *                 workspace must not overlap on the GPU.

@@ -1,6 +1,9 @@
 // C ABI of the cached-decoding operators (include/dd.h): argument validation and launches.
 #include <math.h>
 
+#include <algorithm>
+#include <initializer_list>
+
 #include "dd_common.cuh"
 #include "dd_internal.h"
 
@@ -26,6 +29,49 @@ dd_status check_cache(const dd_paged_cache* c) {
 
 // Slots a table row has room for.
 int64_t table_slots(const dd_paged_cache* c) { return (int64_t)c->max_pages * c->page_size; }
+
+// n rows of `bytes` each, `stride` bytes apart: what a call reads or writes of an argument.
+struct Rows {
+  const void* p;
+  int64_t n, bytes, stride;
+};
+Rows flat(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
+
+using wide = __int128;  // offsets of any strides
+wide floor_div(wide a, wide b) { return a / b - (a % b < 0); }
+
+// Whether a row of x and a row of y have a byte in common. Rows of one may lie between
+// those of the other (columns of a wider table), so the extents alone do not say.
+bool overlap(Rows x, Rows y) {
+  if (!x.p || !y.p) return false;
+  if (x.n > y.n) std::swap(x, y);
+  const auto at = [](const Rows& r) { return (wide) reinterpret_cast<uintptr_t>(r.p); };
+  const auto end = [&](const Rows& r) { return at(r) + (wide)(r.n - 1) * r.stride + r.bytes; };
+  if (end(x) <= at(y) || end(y) <= at(x)) return false;
+  const wide step = y.n > 1 ? y.stride : 1;
+  for (int64_t i = 0; i < x.n; ++i) {  // rows j of y with at + j step in (lo - bytes, lo + x.bytes)
+    const wide lo = at(x) + (wide)i * x.stride - at(y);
+    const wide first = floor_div(lo - y.bytes, step) + 1, last = floor_div(lo + x.bytes - 1, step);
+    if (std::max<wide>(first, 0) <= std::min<wide>(last, y.n - 1)) return true;
+  }
+  return false;
+}
+
+// Whether an output lies in the memory of an input or of another output. CTAs read inputs
+// while others write, so such a call would depend on timing.
+bool clash(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Rows& in : ins)
+      if (overlap(*o, in)) return true;
+    for (auto other = o + 1; other != outs.end(); ++other)
+      if (overlap(*o, *other)) return true;
+  }
+  return false;
+}
+
+Rows table_rows(const dd_paged_cache* c, int64_t n) {
+  return Rows{c->page_table, n, (int64_t)c->max_pages * 4, c->table_stride * 4};
+}
 
 }  // namespace
 
@@ -63,8 +109,16 @@ dd_status dd_paged_attention(const void* q, int64_t q_stride, const void* k_new,
   if (B > kPagedMaxBatch || Hq > kPagedMaxHeads || max_len > kPagedMaxLen) return DD_ERR_UNSUPPORTED;
   if (paged_attention_tiles(B, Hq, max_len) >= (1ll << 31)) return DD_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DD_ERR_INVALID_ARG;
-  if (workspace_bytes <
-      paged_attention_workspace(B, Hq, cache->Hkv, cache->d, max_len, mass_out != nullptr))
+  const size_t need = paged_attention_workspace(B, Hq, cache->Hkv, cache->d, max_len, mass_out != nullptr);
+  if (workspace_bytes < need) return DD_ERR_INVALID_ARG;
+  // in place: a block of heads is written after its queries are read, a mass by its reader
+  const int64_t q_row = (int64_t)Hq * cache->d * e, new_row = (int64_t)cache->Hkv * cache->d * e;
+  const bool in_place = out == q && (B == 1 || q_stride == (int64_t)Hq * cache->d);
+  if (clash({flat(out, B * q_row), flat(lse, (int64_t)B * Hq * 4), Rows{mass_out, B, (int64_t)max_len * 4, mass_stride * 4},
+             flat(workspace, (int64_t)need)},
+            {Rows{in_place ? nullptr : q, B, q_row, q_stride * e}, Rows{k_new, B, new_row, new_stride * e},
+             Rows{v_new, B, new_row, new_stride * e}, flat(lengths, (int64_t)B * 4), table_rows(cache, B),
+             Rows{mass_in == mass_out ? nullptr : mass_in, B, (int64_t)max_len * 4, mass_stride * 4}}))
     return DD_ERR_INVALID_ARG;
   PagedCall p{};
   p.q = q; p.q_stride = B > 1 ? q_stride : 0;
@@ -92,6 +146,11 @@ dd_status dd_cache_evict(const dd_paged_cache* cache, const int32_t* lengths, in
   if (stride < max_len || lengths == lengths_out || mass_in == mass_out || pos_in == pos_out)
     return DD_ERR_INVALID_ARG;
   if (N > 65535 || max_len > kEvictMaxLen) return DD_ERR_UNSUPPORTED;
+  const auto rows = [&](const void* x, int slots) { return Rows{x, N, (int64_t)slots * 4, stride * 4}; };
+  const int left = std::min(budget, max_len);
+  if (clash({rows(mass_out, left), rows(pos_out, left), rows(src_out, left), flat(lengths_out, (int64_t)N * 4)},
+            {rows(mass_in, max_len), rows(pos_in, max_len), flat(lengths, (int64_t)N * 4), table_rows(cache, N)}))
+    return DD_ERR_INVALID_ARG;
   EvictCall p{cache, lengths, N, max_len, budget, sink, recent, mass_in, pos_in, stride,
               mass_out, pos_out, src_out, lengths_out};
   return from_cuda(launch_cache_evict(p, static_cast<cudaStream_t>(stream)));
@@ -116,7 +175,13 @@ dd_status dd_beam_select(const void* logits, dd_dtype dtype, int B, int K, int V
   if (K > kBeamMaxK || V > kBeamMaxV || (int64_t)B * K > (1ll << 20)) return DD_ERR_UNSUPPORTED;
   if ((int64_t)B * K * ((V + 4095) / 4096) >= (1ll << 31)) return DD_ERR_UNSUPPORTED;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return DD_ERR_INVALID_ARG;
-  if (workspace_bytes < beam_select_workspace(B, K, V, dtype)) return DD_ERR_INVALID_ARG;
+  const size_t need = beam_select_workspace(B, K, V, dtype);
+  if (workspace_bytes < need) return DD_ERR_INVALID_ARG;
+  const int64_t n = (int64_t)B * K, e = (int64_t)elem_size(dtype);
+  if (clash({flat(parent, n * 4), flat(token, n * 4), flat(score_out, n * 4), flat(done_out, n),
+             flat(workspace, (int64_t)need)},
+            {Rows{logits, n, V * e, ld * e}, flat(score_in, n * 4), flat(done_in, n)}))
+    return DD_ERR_INVALID_ARG;
   BeamCall p{logits, dtype, B, K, V, ld, score_in, done_in, eos, parent, token, score_out,
              done_out, workspace};
   return from_cuda(launch_beam_select(p, static_cast<cudaStream_t>(stream)));
@@ -132,6 +197,17 @@ dd_status dd_beam_reorder(const int32_t* parent, int B, int K, const dd_row_stat
     if ((int64_t)B * K > 1 && (s.src_stride < s.row_bytes || s.dst_stride < s.row_bytes))
       return DD_ERR_INVALID_ARG;
   }
+  const int64_t n = (int64_t)B * K;
+  for (int i = 0; i < n_states; ++i) {
+    const Rows dst{states[i].dst, n, states[i].row_bytes, states[i].dst_stride};
+    if (overlap(dst, flat(parent, n * 4))) return DD_ERR_INVALID_ARG;
+    for (int j = 0; j < n_states; ++j) {
+      const dd_row_state& s = states[j];
+      if (overlap(dst, Rows{s.src, n, s.row_bytes, s.src_stride}) ||
+          (j > i && overlap(dst, Rows{s.dst, n, s.row_bytes, s.dst_stride})))
+        return DD_ERR_INVALID_ARG;
+    }
+  }
   return from_cuda(
       launch_beam_reorder(parent, B, K, states, n_states, static_cast<cudaStream_t>(stream)));
 }
@@ -145,6 +221,10 @@ dd_status dd_paged_fork(const dd_paged_cache* cache, const int32_t* parent, int 
   if (B < 1 || K < 1 || out_stride < cache->max_pages) return DD_ERR_INVALID_ARG;
   if (table_out == cache->page_table || lengths_out == lengths) return DD_ERR_INVALID_ARG;
   if ((int64_t)B * K > 65535) return DD_ERR_UNSUPPORTED;
+  const int64_t n = (int64_t)B * K;
+  if (clash({Rows{table_out, n, (int64_t)cache->max_pages * 4, out_stride * 4}, flat(lengths_out, n * 4)},
+            {table_rows(cache, n), flat(parent, n * 4), flat(lengths, n * 4), flat(fresh, n * 4)}))
+    return DD_ERR_INVALID_ARG;
   return from_cuda(launch_paged_fork(*cache, parent, B, K, lengths, fresh, table_out, out_stride,
                                      lengths_out, static_cast<cudaStream_t>(stream)));
 }

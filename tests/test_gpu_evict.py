@@ -204,3 +204,15 @@ def test_refusals_of_the_binding():
                  dict(max_len=100), dict(recent=-1)):
         with pytest.raises(dd.DDError):
             call(**over)
+
+
+def test_outputs_in_other_arguments_memory_are_refused():
+    k, v, table, mass, pos = _case(30, N=2, page=16, Hkv=1, d=64, lengths=[60, 60])
+    cache, mass, pos = dd.PagedCache(k, v, table.cuda()), mass.cuda(), pos.cuda()
+    lens = torch.tensor([60, 60], dtype=torch.int32, device="cuda")
+    mo, po = torch.zeros_like(mass), torch.zeros_like(pos)
+    for over in (dict(src=pos), dict(src=po), dict(pos_out=mass.view(torch.int32)), dict(lengths_out=pos[0, 5:7])):
+        a = dict(pos_out=po, lengths_out=torch.zeros_like(lens))
+        a.update(over)
+        with pytest.raises(dd.DDError):
+            dd.dd_cache_evict(cache, lens, mass, pos, 30, mo, **a)

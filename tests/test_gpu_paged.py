@@ -351,3 +351,39 @@ def test_masses_of_short_sequences(dtype, B, Hq, Hkv, lengths):
     lengths = (lengths * B)[:B]
     holes = [(b, 0) for b in range(0, B, 7) if lengths[b] > 8]
     _check(24, B=B, Hq=Hq, Hkv=Hkv, d=64, page=8, lengths=lengths, dtype=dtype, mass=True, holes=holes)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lengths", [[700, 31, 512, 0], [50, 64, 1, 0], [300], [200, 5, 0, 64, 129] * 12])
+@pytest.mark.parametrize("mass", [False, True])
+def test_outputs_beside_and_in_place_of_inputs(dtype, lengths, mass):
+    """The output in the queries' place, and masses in columns between each other's: the same bits."""
+    x = CC.make_attention(50, B=len(lengths), Hq=40, Hkv=4, d=64, page=16, lengths=lengths, mass=mass, dtype=dtype)
+    want = CC.run_attention(CC.on_gpu(x))
+    g = CC.on_gpu(x)
+    B, M = len(lengths), x["max_len"] + 3
+    both = torch.full((B, 2, M), 7.0, device="cuda")
+    kw = {}
+    if mass:
+        both[:, 0] = g["mass"]
+        both[:, 1] = g["mass"]
+        kw = dict(mass=both[:, 0], mass_out=both[:, 1])
+    dd.dd_paged_attention(g["q"], dd.PagedCache(g["k"], g["v"], g["table"]), g["lengths"], g["q"], k_new=g["k_new"],
+                          v_new=g["v_new"], max_len=x["max_len"], **kw)
+    torch.cuda.synchronize()
+    assert dd.dd_get_device_error() == dd.DD_OK
+    assert torch.equal(g["q"], want["out"])
+    if mass:
+        assert torch.equal(both[:, 1], want["mass"]) and torch.equal(both[:, 0], g["mass"])
+
+
+def test_overlapping_outputs_are_refused():
+    x = CC.make_attention(51, B=2, Hq=4, Hkv=2, d=64, page=16, lengths=[20, 30], mass=True)
+    g = CC.on_gpu(x)
+    cache = dd.PagedCache(g["k"], g["v"], g["table"])
+    buf = torch.zeros(4096, device="cuda")
+    q = buf[:512].view(BF16)[:512].view(2, 4, 64)
+    for kw in (dict(out=buf.view(BF16)[8:520].view(2, 4, 64)), dict(out=g["k_new"].new_zeros(2, 4, 64), lse=buf[:8].view(2, 4)),
+               dict(out=torch.zeros_like(q), mass=buf[600:666].view(2, 33), mass_out=buf[601:667].view(2, 33))):
+        with pytest.raises(dd.DDError):
+            dd.dd_paged_attention(q, cache, g["lengths"], kw.pop("out"), max_len=30, **kw)
