@@ -93,7 +93,8 @@ class BudgetedCache:
 class BeamDecode:
     def __init__(self, k, v, Hq, K, vocab, steps, page_size=16, eos=-1):
         """k, v [layers,B,L,Hkv,d]: the prompts' caches, one beam each; K beams and at most
-        `steps` tokens from there on."""
+        `steps` tokens (begin) and `steps` choices (advance) from there on, in any order: the
+        first choice may come from the prompts' own logits, before any token."""
         layers, B, L, Hkv, d = k.shape
         dev, dtype, N = k.device, k.dtype, B * K
         i32 = dict(dtype=torch.int32, device=dev)
@@ -126,7 +127,8 @@ class BeamDecode:
         self.ws = torch.empty(max(
             dd.dd_paged_attention_workspace_size(N, Hq, Hkv, d, width * page_size),
             dd.dd_beam_select_workspace_size(B, K, vocab, torch.float32)), dtype=torch.uint8, device=dev)
-        self.t = 0
+        self.t = 0        # choices so far
+        self._slots = L   # a beam's slots
         # the prompts: full pages shared by a request's beams, the rest in each beam's own page
         page = page_size
         if shared:
@@ -136,21 +138,27 @@ class BeamDecode:
             self.table[:, :shared] = ids.repeat_interleave(K, 0)
         own = self._fresh()
         self.table[:, shared] = own
+        self._open = shared  # the last page a beam has
         rest = L - shared * page
         for pool, x in ((self.pool_k, k), (self.pool_v, v)):
             pool[:, own.long(), :rest] = x[:, :, shared * page:].repeat_interleave(K, 1)
 
     def _fresh(self):
-        """The page each beam goes on in after this step's fork."""
+        """The page each beam goes on in: one of the two of the page its next slot lies in."""
         page = self.caches[0].page_size
-        i = (self.L + self.t) // page - self.L // page
+        i = self._slots // page - self.L // page
         return self._first + 2 * (i * self.N + self._own) + self.t % 2
 
     def begin(self):
         """A new token for every beam: its slot counts from here on."""
-        if self.t >= self.steps:
+        if self._slots - self.L >= self.steps:
             raise ValueError(f"all {self.steps} steps are taken")
+        page = self._slots // self.caches[0].page_size
+        if page > self._open:  # the last token filled a page, and no fork gave a next one
+            self.table[:, page] = self._fresh()
+            self._open = page
         self.lengths += 1
+        self._slots += 1
 
     def attend(self, layer, q, k_new, v_new):
         """One layer: q [N,Hq,d], k_new, v_new [N,Hkv,d] of the beams' current tokens."""
@@ -160,7 +168,10 @@ class BeamDecode:
 
     def advance(self, logits):
         """logits [B,K,V] of the beams: selects, and moves every state to its new beam. The
-        chosen tokens [B,K] are what the beams' next step embeds."""
+        chosen tokens [B,K] are what the beams' next step embeds (-1: no candidate was left for
+        that beam, its score is -inf)."""
+        if self.t >= self.steps:
+            raise ValueError(f"all {self.steps} steps are taken")
         dd.dd_beam_select(logits, self.score, self.parent, self.token, self._score_out,
                           done=self.done, done_out=self._done_out, eos=self.eos, workspace=self.ws)
         dd.dd_beam_reorder(self.parent, [(self.tokens, self._tokens_out)])
@@ -169,6 +180,7 @@ class BeamDecode:
         self.t += 1
         dd.dd_paged_fork(self.caches[0], self.parent, self.lengths, self._fresh(), self._table_out,
                          self._lengths_out)
+        self._open = self._slots // self.caches[0].page_size
         self.table, self._table_out = self._table_out, self.table
         self.caches.reverse()
         self._layers.reverse()

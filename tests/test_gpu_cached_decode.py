@@ -9,6 +9,7 @@ from oracle import cached as OC
 from speculative_verification_cover_b200 import dd
 from speculative_verification_cover_b200.cached_decode import BeamDecode, BudgetedCache
 from tests import cached_cases as CC
+from tests.test_cached_compose import PATTERNS, beams_hold_their_histories
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +139,10 @@ def test_prompt_masses_from_the_verification_attention():
     dd.dd_paged_attention(q[:, 5].contiguous(), dd.PagedCache(k, v, table), n, o, z)
     assert torch.allclose(o.float(), out[:, 5].float(), atol=2e-2)
     assert torch.allclose(z, lse[:, :, 5], atol=1e-3)
+
+
+@pytest.mark.parametrize("pattern", PATTERNS)
+@pytest.mark.parametrize("page,L", [(1, 3), (2, 4), (3, 9), (16, 5)])
+def test_beams_hold_their_own_histories(pattern, page, L):
+    beams_hold_their_histories(pattern, page, L, "cuda")
+    assert dd.dd_get_device_error() == dd.DD_OK
