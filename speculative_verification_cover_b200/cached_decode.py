@@ -26,6 +26,10 @@ class BudgetedCache:
                  prompt=0, dtype=torch.bfloat16, device="cuda"):
         """budget: slots a sequence keeps; every: tokens between evictions (the cache has room
         for budget + every slots); prompt: the longest prompt, if it is above the budget."""
+        if budget < 1 or every < 1 or prompt < 0:
+            raise ValueError(f"budget {budget} and every {every} must be positive, prompt {prompt} not negative")
+        if sink < 0 or recent < 0 or sink + recent > budget:
+            raise ValueError(f"sink {sink} and recent {recent} must fit into the budget of {budget} slots")
         cap = max(budget + every, prompt)
         width = _pages(cap, page_size)
         self.N, self.Hq, self.budget, self.every = N, Hq, budget, every
@@ -50,7 +54,8 @@ class BudgetedCache:
 
     def fill(self, k, v, mass=None, lengths=None):
         """A prompt: k, v [N,L,Hkv,d]; mass [N,L] its first masses (dd_dualview_attention's
-        d_in, say; None: zero); lengths [N] its lengths (None: L)."""
+        d_in, say; None: zero); lengths [N] its lengths (None: L; values outside 0 .. L are
+        clamped)."""
         N, L = k.shape[:2]
         if L > self.cache.slots:
             raise ValueError(f"a prompt of {L} slots, room for {self.cache.slots}")
@@ -63,7 +68,8 @@ class BudgetedCache:
         if mass is not None:
             self.mass[:, :L] = mass
         self.pos[:, :L] = slots.to(torch.int32)
-        self.lengths.fill_(L) if lengths is None else self.lengths.copy_(lengths)
+        # what attend() makes slot indexes of: no length may lie behind the rows
+        self.lengths.fill_(L) if lengths is None else self.lengths.copy_(lengths.clamp(0, L))
         self.seen.copy_(self.lengths)
         self._most = L
         if L > self.budget:

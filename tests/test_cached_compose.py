@@ -6,7 +6,7 @@ import torch
 
 from oracle import cached as OC
 from speculative_verification_cover_b200 import build, dd
-from speculative_verification_cover_b200.cached_decode import BeamDecode
+from speculative_verification_cover_b200.cached_decode import BeamDecode, BudgetedCache
 
 
 def _attention(q, cache, lengths, out, lse=None, k_new=None, v_new=None, **kw):
@@ -95,3 +95,31 @@ def test_beams_hold_their_own_histories(played, pattern, page, L):
     """Whatever the order of new tokens (begin, attend) and choices (advance): a prompt's logits
     may be chosen from before the first token, and tokens may follow each other unbranched."""
     beams_hold_their_histories(pattern, page, L, "cpu")
+
+
+def test_budgets_and_lengths_out_of_range(played, monkeypatch):
+    """What would send a slot's position behind its row is refused, or clamped as the library
+    clamps lengths."""
+    make = lambda **kw: BudgetedCache(**(dict(N=3, Hq=2, Hkv=1, d=64, budget=16, page_size=4, sink=2, recent=6,
+                                              device="cpu", dtype=torch.float32) | kw))
+    for kw in (dict(every=0), dict(every=-1), dict(budget=0), dict(budget=7), dict(sink=-1), dict(recent=-1),
+               dict(sink=4, recent=13), dict(prompt=-1)):
+        with pytest.raises(ValueError):
+            make(**kw)
+    make(budget=8), make(sink=16, recent=0)
+    evicted = []
+
+    def evict(cache, lengths, mass, pos, budget, mass_out, pos_out, lengths_out, **kw):
+        evicted.append(lengths.tolist())
+        mass_out.copy_(mass), pos_out.copy_(pos), lengths_out.copy_(lengths.clamp(max=budget))
+
+    monkeypatch.setattr(dd, "dd_cache_evict", evict)
+    c = make(every=2)
+    k, q, new = torch.randn(3, 10, 1, 64), torch.zeros(3, 2, 64), torch.randn(3, 1, 64)
+    c.fill(k, k, lengths=torch.tensor([-4, 1000, 7], dtype=torch.int32))
+    assert c.lengths.tolist() == c.seen.tolist() == [0, 10, 7]
+    for t in range(12):
+        c.attend(q, new, new)
+        n = c.lengths.tolist()
+        assert max(n) <= c.cache.slots and c.pos[1, n[1] - 1] == 10 + t and c.pos[0, n[0] - 1] == t
+    assert evicted == [[8, 18, 15], [10, 18, 17]]
