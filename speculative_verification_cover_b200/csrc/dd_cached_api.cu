@@ -30,32 +30,36 @@ dd_status check_cache(const dd_paged_cache* c) {
 // Slots a table row has room for.
 int64_t table_slots(const dd_paged_cache* c) { return (int64_t)c->max_pages * c->page_size; }
 
-// n rows of `bytes` each, `stride` bytes apart: what a call reads or writes of an argument.
-struct Rows {
-  const void* p;
-  int64_t n, bytes, stride;
-};
-Rows flat(const void* p, int64_t bytes) { return Rows{p, 1, bytes, bytes}; }
-
 using wide = __int128;  // offsets of any strides
 wide floor_div(wide a, wide b) { return a / b - (a % b < 0); }
 
-// Whether a row of x and a row of y have a byte in common. Rows of one may lie between
-// those of the other (columns of a wider table), so the extents alone do not say.
-bool overlap(Rows x, Rows y) {
-  if (!x.p || !y.p) return false;
-  if (x.n > y.n) std::swap(x, y);
-  const auto at = [](const Rows& r) { return (wide) reinterpret_cast<uintptr_t>(r.p); };
-  const auto end = [&](const Rows& r) { return at(r) + (wide)(r.n - 1) * r.stride + r.bytes; };
-  if (end(x) <= at(y) || end(y) <= at(x)) return false;
+// n rows of `bytes` each, `stride` bytes apart: what a call reads or writes of an argument.
+struct Rows {
+  uintptr_t at, end;  // all of them lie in [at, end); empty where there is none
+  int64_t n, bytes, stride;
+  Rows(const void* p, int64_t rows, int64_t row_bytes, int64_t row_stride)
+      : at(reinterpret_cast<uintptr_t>(p)), end(at), n(rows), bytes(row_bytes), stride(row_stride) {
+    int64_t extent;
+    if (p && (__builtin_mul_overflow(n - 1, stride, &extent) || __builtin_add_overflow(extent, bytes, &extent) ||
+              __builtin_add_overflow(at, (uintptr_t)extent, &end)))
+      end = UINTPTR_MAX;
+  }
+};
+Rows flat(const void* p, int64_t bytes) { return Rows(p, 1, bytes, bytes); }
+
+// Whether a row of x and a row of y, whose extents meet, have a byte in common: rows of one
+// may lie between those of the other (columns of a wider table).
+bool rows_meet(const Rows& x, const Rows& y) {
+  if (x.n > y.n) return rows_meet(y, x);
   const wide step = y.n > 1 ? y.stride : 1;
-  for (int64_t i = 0; i < x.n; ++i) {  // rows j of y with at + j step in (lo - bytes, lo + x.bytes)
-    const wide lo = at(x) + (wide)i * x.stride - at(y);
+  for (int64_t i = 0; i < x.n; ++i) {  // rows j of y with j step in (lo - y.bytes, lo + x.bytes)
+    const wide lo = (wide)x.at + (wide)i * x.stride - (wide)y.at;
     const wide first = floor_div(lo - y.bytes, step) + 1, last = floor_div(lo + x.bytes - 1, step);
     if (std::max<wide>(first, 0) <= std::min<wide>(last, y.n - 1)) return true;
   }
   return false;
 }
+bool overlap(const Rows& x, const Rows& y) { return x.at < y.end && y.at < x.end && rows_meet(x, y); }
 
 // Whether an output lies in the memory of an input or of another output. CTAs read inputs
 // while others write, so such a call would depend on timing.
@@ -70,7 +74,7 @@ bool clash(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
 }
 
 Rows table_rows(const dd_paged_cache* c, int64_t n) {
-  return Rows{c->page_table, n, (int64_t)c->max_pages * 4, c->table_stride * 4};
+  return Rows(c->page_table, n, (int64_t)c->max_pages * 4, c->table_stride * 4);
 }
 
 }  // namespace
