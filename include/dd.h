@@ -465,7 +465,9 @@ size_t dd_paged_attention_workspace_size(int B, int Hq, int Hkv, int d, int max_
  * src_out         [N, .] int32, stride `stride`, or NULL: the old slot of each new one (to
  *                 move whatever else a program keeps per slot)
  * lengths_out     [N] int32 = min(lengths, budget), not the memory of `lengths`
- * A slot in a hole moves nothing (its row stays as it is); mass and position follow.
+ * A slot in a hole moves nothing: what lay in the slot it moves to stays there, under the
+ * mover's mass and position (a program that drops pages gives their slots the lowest mass,
+ * so that they go first).
  * Errors: DD_ERR_INVALID_ARG for null pointers, sizes or strides out of range,
  * budget < 1, sink or recent < 0, sink + recent > budget, outputs that are the inputs'
  * memory; DD_ERR_UNSUPPORTED for d not in {64,128}, N > 65535 or max_len > 524288.

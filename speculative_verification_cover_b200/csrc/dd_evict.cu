@@ -91,7 +91,7 @@ struct Crossing {
 };
 template <typename F>
 __device__ Crossing find_bin(int bins, int want, int* warp_tmp, int* found, F counts) {
-  const int per = (bins + blockDim.x - 1) / blockDim.x;  // at most 8: 2048 bins, 256 threads
+  const int per = (bins + blockDim.x - 1) / blockDim.x;  // at most 8: 2048 bins, 256 threads; 4096, 512
   const int first = (int)threadIdx.x * per;              // counted from the top
   int c[8], sum = 0;
 #pragma unroll
@@ -226,7 +226,7 @@ __device__ void write_slots(const EvictArgs& a, int n, int begin, int end, MoveL
 // of keys to rank by counting (a bin of more than kEvictList gets another histogram). Kept
 // slots become a bitmap, and the i-th freed slot below the new length takes the i-th kept
 // slot at or beyond it: both are ranks over the bitmap (one prefix count per word and a bit
-// count). Bound: the latency of its steps: 7.0 us for 16 sequences of 1025 slots of 8 heads of
+// count). Bound: the latency of its steps: 7.2 us for 16 sequences of 1025 slots of 8 heads of
 // 128, one leaving each.
 __global__ void __launch_bounds__(kEvictFew)
 evict_short_kernel(const __grid_constant__ EvictArgs a) {
@@ -355,7 +355,7 @@ evict_short_kernel(const __grid_constant__ EvictArgs a) {
 // several clusters repeat a selection and share the moves.
 // Bound: the chain of about ten steps, 2 to 7 K cycles each (7 cluster barriers among them),
 // and the rows that move: 16 sequences of up to 8192 slots, 4 heads of 128 bf16, cut to 1024
-// (46 MB): 20.6 us; one of 30001 cut to 9999: 20.7 us. A CTA for each sequence took 70 and 115.
+// (46 MB): 20.0 us; one of 30001 cut to 9999: 20.7 us. A CTA for each sequence took 70 and 115.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kEvictMany)
 evict_cluster_kernel(const __grid_constant__ EvictArgs a) {
   namespace cg = cooperative_groups;

@@ -14,9 +14,9 @@
 // depends on max_len.
 //
 // Bound: HBM, 2 Hkv d elements per slot read once. Measured (one B200, calls in a graph; of
-// the copy bandwidth): one sequence of 131071 slots, 8 kv heads of 128 bf16, 89 us (92%); 64
-// sequences of up to 8191, 4 kv heads, with masses, 111 us (75%; the scores' way to the join
-// and back is 58 of 600 MB); 7 of up to 2047, 32 kv heads, 26.6 us (71%): there the first
+// the copy bandwidth): one sequence of 131071 slots, 8 kv heads of 128 bf16, 86.9 us (95%); 64
+// sequences of 17 to 8191, 4 kv heads, with masses, 110.4 us (75%; the scores' way to the join
+// and back is 58 of 600 MB); 7 of 101 to 2047, 32 kv heads, 26.5 us (71%): there the first
 // lengths, page ids and slots arriving, and the ends of sequence-heads, are a third of it.
 #include <cooperative_groups.h>
 
@@ -679,8 +679,9 @@ __device__ __forceinline__ LaneRow<float, N> load_vec(const float* p) {
 // rather than 5 U GB, and the product of (slot u, head g) ends in the lanes whose top
 // bits are u GB + g. Softmax and mass scores are then one value per lane.
 // Bound: HBM while a kv head has few query heads (16 sequences of 2000 to 4000 slots, 8 kv
-// heads of 128, 4 query heads each: 68 us, 89% of the copy bandwidth); at 8 its issue slots
-// (8000 slots, 4 kv heads of 64: 66 us, 46%).
+// heads of 128: 1 or 4 query heads each 68 us, 89% of the copy bandwidth); at 8 its issue slots
+// (the same: 89 us, 68%; 12 sequences of 8000 slots, 4 kv heads of 64: 64 us, 47%). More than 8
+// are blocks of up to 8 that each read the cache (16: 169 us, 36%).
 template <typename C, int D, int GB, bool CL>
 __global__ void __launch_bounds__(kPagedThreads, C::kCtas)
 paged_fp32_kernel(const __grid_constant__ PagedArgs a) {
@@ -1124,7 +1125,10 @@ cudaError_t launch_fp32_heads(PagedArgs& a, cudaStream_t stream) {
 // which one long sequence wants (bf16, 131071 slots, 8 kv heads: 88.7 us, against 92.9 with
 // three CTAs of two stages). Where there are as many sequence-heads as SMs their ends and
 // starts cost more, and a third CTA works through them (7 sequences of 32 kv heads: 26.9 us
-// against 29.0; 64 of 4: 109.5 against 111.0).
+// against 29.0; 64 of 4: 109.5 against 111.0). Both sides of each were measured in one run.
+// 9 to 16 query heads leave registers for two CTAs, and two stages at d = 128: 32 sequences of
+// 4096 slots, 4 kv heads of 128, take 54.5 us with 9 and 56.8 with 16, 51.4 with 8 (75, 72 and
+// 80% of the copy bandwidth); with 8 kv heads of 64, 16 query heads each, 78 us (53%).
 template <int D>
 cudaError_t launch_bf16(PagedArgs& a, cudaStream_t stream) {
   using T = __nv_bfloat16;
